@@ -261,6 +261,115 @@ DG_API dg_status dg_cast_fp8_per_block_ue8m0(const void *x, void *q, uint32_t *s
  *   not written). T % 128 == 0, C % 8 == 0, else DG_ERR_INVALID_ARG. */
 DG_API dg_status dg_cast_fp8_per_channel(const void *x, void *q, float *sf, int T, int C, void *stream);
 
+/* Element types of the operators below that take more than one. */
+typedef enum dg_dtype { DG_BF16 = 0, DG_FP32 = 1 } dg_dtype;
+
+/* Layer norm (rms = 0) or RMS norm (rms != 0) over the K elements of each row, with the
+ * per-token FP8 cast of the result as an option (the pages fuse such casts into the producing
+ * kernel; likun.im §五 gives the scales' layout):
+ *   mu = mean(x) (0 for rms), r = 1/sqrt(mean((x-mu)^2) + eps), y = (x-mu)·r·weight + bias.
+ *   x       [T,K] of x_type (DG_BF16 or DG_FP32)
+ *   weight, bias  [K] of w_type, or NULL (ones, zeros); rms takes no bias
+ *   y       [T,K] of x_type, or NULL when only the codes are wanted; may be x itself
+ *   q, sfa  e4m3 [T,K] and fp32 [Kb][pad4(T)] by the rule of dg_cast_fp8_per_token, or both NULL;
+ *           the cast is of the fp32 y before its rounding to x_type; padding entries of sfa are
+ *           not written. Needs K % 128 == 0.
+ *   mean, rstd  fp32 [T], what dg_layer_norm_backward reads, or NULL.
+ * Any K from 1 to 32768, eps >= 0. Statistics are fp32. */
+DG_API dg_status dg_layer_norm(const void *x, const void *weight, const void *bias, void *y, void *q, float *sfa,
+                               float *mean, float *rstd, int T, int K, float eps, int rms, int x_type, int w_type,
+                               void *stream);
+
+/* Gradients of dg_layer_norm's y, with xh = (x-mean)·rstd and u = dy·weight:
+ *   dx = rstd·(u - mean_K(u) - xh·mean_K(u·xh))  (mean = NULL, the RMS form: without mean_K(u));
+ *   dw = sum over rows of dy·xh, db = sum over rows of dy: fp32 [K], either may be NULL. With
+ *   T = 0 they are zeroed.
+ *   dy, x, dx  [T,K] of x_type; weight [K] of w_type or NULL; mean, rstd as the forward wrote them.
+ *   workspace  dg_layer_norm_backward_workspace(T, K) bytes of device memory, 16-byte aligned, for
+ *              this call alone until its work on the stream is done; NULL when dw and db are.
+ * dx may not overlap dy or x. The sums over rows are taken in a fixed order. */
+DG_API dg_status dg_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean,
+                                        const float *rstd, void *dx, float *dw, float *db, void *workspace,
+                                        long long workspace_bytes, int T, int K, int x_type, int w_type, void *stream);
+DG_API long long dg_layer_norm_backward_workspace(int T, int K);
+
+/* Routing of tokens to experts, in front of the grouped GEMMs. For a token with logits x[E]:
+ *   s = softmax(x) or sigmoid(x); choice values c = s + bias (bias may be NULL);
+ *   the E experts form `groups` groups of E/groups; a group's value is the sum of its group_top
+ *   (1 or 2) largest c, and the topk_groups groups of largest value are kept;
+ *   ids = the k experts of largest c in the kept groups, in falling order of c;
+ *   w_j = s[ids_j], divided by their sum if renorm, times scale. The bias is in no weight.
+ * Equal values are taken in the order of their index. The choice follows the real values: scores
+ * that differ by less than an fp32 rounding are not confused. A logit of -inf or a bias of -inf
+ * takes the expert out of the choice; so does a NaN, which also sets the device error word; a
+ * logit of +inf counts as the largest finite fp32. Where fewer than k experts are left, the last
+ * ids are -1 and their weights 0. A group with fewer than group_top experts left counts those
+ * it has.
+ *   logits  [T,E] of dtype (DG_BF16 or DG_FP32);  bias fp32 [E] or NULL
+ *   ids     int32 [T,k];  weights fp32 [T,k]
+ * Limits: E <= 1024, k <= min(E, 32), groups <= 32 and E % groups == 0. */
+typedef enum dg_score { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 } dg_score;
+DG_API dg_status dg_moe_route(const void *logits, const float *bias, int32_t *ids, float *weights, int T, int E, int k,
+                              int groups, int topk_groups, int group_top, int score, int renorm, float scale, int dtype,
+                              void *stream);
+
+/* Gradient of the logits from the gradient of dg_moe_route's weights (fp32 [T,k]). ids are the
+ * forward's; -1 (any negative id) has no gradient, an id >= E sets the device error word and is
+ * left out, an id that stands twice in a row gets both gradients. grad_logits [T,E] of dtype is
+ * written in full; it may not overlap logits. score, renorm and scale are the forward's. */
+DG_API dg_status dg_moe_route_backward(const float *grad_weights, const void *logits, const int32_t *ids,
+                                       void *grad_logits, int T, int E, int k, int score, int renorm, float scale,
+                                       int dtype, void *stream);
+
+/* Rows of the grouped layouts for the expert ids of T tokens (int32 [T,k]; ids outside [0,G),
+ * such as -1 or another rank's experts, are dropped: row -1). Rows follow the order of the pairs
+ * (token, then place), so they are the same in every run.
+ *   contiguous: expert g's rows start where the earlier experts' rows, each padded to a multiple
+ *     of 128, end. dst_rows int32 [T,k]; grouped_layout int32 [M_sum] as
+ *     dg_m_grouped_fp8_gemm_nt_contiguous reads it (-1 for padding and all rows behind the last
+ *     expert); ks int32 [G], the padded row counts (ks_device of the K-grouped GEMM), or NULL.
+ *     M_sum % 128 == 0; T·k + 127·min(G, T·k), rounded up to a multiple of 128, fits any ids.
+ *   masked: expert g's rows are g·M_max, g·M_max + 1, ...; masked_m int32 [G], their number.
+ * A pair whose row would lie outside M_sum (or at or behind M_max) gets row -1 and sets the device
+ * error word; ks and masked_m are clamped.
+ *   workspace  dg_moe_layout_workspace(T, k, G) bytes of device memory (0 for up to 2048 pairs),
+ *              16-byte aligned, for this call alone until its work on the stream is done.
+ * Limits: G <= 1024, T·k <= 2^30, G·M_max < 2^31. */
+DG_API dg_status dg_moe_layout_contiguous(const int32_t *ids, int32_t *dst_rows, int32_t *grouped_layout, int32_t *ks,
+                                          void *workspace, long long workspace_bytes, int T, int k, int G, int M_sum,
+                                          void *stream);
+DG_API dg_status dg_moe_layout_masked(const int32_t *ids, int32_t *dst_rows, int32_t *masked_m, void *workspace,
+                                      long long workspace_bytes, int T, int k, int G, int M_max, void *stream);
+DG_API long long dg_moe_layout_workspace(int T, int k, int G);
+
+/* dg_cast_fp8_per_token_scatter for k rows per token and both grouped layouts: token t is
+ * quantised once and written to the rows dst_rows[t][0..k-1] (int32 [T,k]; negative: none) of G
+ * groups of M rows:
+ *   contiguous: G = 1, M = M_sum;   masked: G experts of M = M_max rows
+ *   q e4m3 [G·M,K];  sfa fp32 [G][Kb][pad4(M)]. Rows no token maps to are not written.
+ * No two pairs may share a row. A row >= G·M sets the device error word and is left out.
+ * K % 128 == 0, G·M < 2^31, T·k <= 2^30. */
+DG_API dg_status dg_cast_fp8_per_token_scatter_topk(const void *x, const int32_t *dst_rows, void *q, float *sfa, int T,
+                                                    int k, int G, int M, int K, void *stream);
+
+/* The experts' results back to the tokens: y[t] = c[t] + sum_j weights[t,j]·d[dst_rows[t,j]].
+ *   d  bf16 [R,N] (R = M_sum, or G·M_max);  dst_rows int32 [T,k] (negative: left out; its row is
+ *   not read);  weights fp32 [T,k] or NULL (ones: also the gradient of the dispatch);
+ *   c  bf16 [T,N] or NULL (may be y);  y bf16 [T,N]. Sums are fp32 in the order of j, rounded once.
+ * N % 8 == 0, k <= 32. A row >= R sets the device error word and is left out. */
+DG_API dg_status dg_moe_combine(const void *d, const int32_t *dst_rows, const float *weights, const void *c, void *y,
+                                int T, int k, int N, int R, void *stream);
+
+/* Gradients of dg_moe_combine: grad_d[dst_rows[t,j]] = weights[t,j]·grad_y[t] (bf16 [R,N]) and
+ * grad_weights[t,j] = <grad_y[t], d[dst_rows[t,j]]> (fp32 [T,k], 0 for a negative row). Either may be
+ * NULL; d is read for grad_weights only. (The gradient of c is grad_y.) No two pairs may share a
+ * row. Rows of grad_d that no pair maps to are not written, except that with grouped_layout
+ * (int32 [R] or NULL) the rows whose entry is negative are zeroed, as the K-grouped weight
+ * gradient wants its padding. grad_d may not overlap d. */
+DG_API dg_status dg_moe_combine_backward(const void *grad_y, const void *d, const int32_t *dst_rows,
+                                         const float *weights, const int32_t *grouped_layout, void *grad_d,
+                                         float *grad_weights, int T, int k, int N, int R, void *stream);
+
 /* pad4(mn): the leading dimension of an MN-major scale array. */
 DG_API int dg_sf_ld(int mn);
 

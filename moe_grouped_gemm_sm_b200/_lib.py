@@ -45,7 +45,7 @@ def load():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m moe_grouped_gemm_sm_b200.build` (nvcc, sm_100a)")
         L = ctypes.CDLL(LIB_PATH)
-        P, I = ctypes.c_void_p, ctypes.c_int
+        P, I, F, Q = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
         sig = {
             "dg_fp8_gemm_nt": [P, P, P, P, P, P, I, I, I, P],
             "dg_fp8_gemm_nt_noalloc": [P, P, P, P, P, P, I, I, I, P],
@@ -66,6 +66,17 @@ def load():
             "dg_fp8_gemm_tn": [P, P, P, P, P, P, I, I, I, P],
             "dg_fp8_gemm_tt": [P, P, P, P, P, P, I, I, I, P],
             "dg_k_grouped_fp8_gemm_tn_contiguous": [P, P, P, P, P, P, P, P, I, I, I, P],
+            "dg_layer_norm": [P, P, P, P, P, P, P, P, I, I, F, I, I, I, P],
+            "dg_layer_norm_backward": [P, P, P, P, P, P, P, P, P, Q, I, I, I, I, P],
+            "dg_layer_norm_backward_workspace": [I, I],
+            "dg_moe_route": [P, P, P, P, I, I, I, I, I, I, I, I, F, I, P],
+            "dg_moe_route_backward": [P, P, P, P, I, I, I, I, I, F, I, P],
+            "dg_moe_layout_contiguous": [P, P, P, P, P, Q, I, I, I, I, P],
+            "dg_moe_layout_masked": [P, P, P, P, Q, I, I, I, I, P],
+            "dg_moe_layout_workspace": [I, I, I],
+            "dg_cast_fp8_per_token_scatter_topk": [P, P, P, P, I, I, I, I, I, P],
+            "dg_moe_combine": [P, P, P, P, P, I, I, I, I, P],
+            "dg_moe_combine_backward": [P, P, P, P, P, P, P, I, I, I, I, P],
             "dg_last_kernel": [],
             "dg_last_launch_count": [],
             "dg_allocated_bytes": [],
@@ -74,7 +85,8 @@ def load():
             f = getattr(L, name)
             f.argtypes = args
             f.restype = {"dg_status_string": ctypes.c_char_p, "dg_last_kernel": ctypes.c_char_p,
-                         "dg_allocated_bytes": ctypes.c_longlong}.get(name, I)
+                         "dg_allocated_bytes": Q, "dg_moe_layout_workspace": Q,
+                         "dg_layer_norm_backward_workspace": Q}.get(name, I)
         _lib = L
     return _lib
 
@@ -171,6 +183,60 @@ def dg_cast_fp8_per_block_ue8m0(x, q, sfb, batch, N, K, stream=None):
 
 def dg_cast_fp8_per_channel(x, q, sf, T, C, stream=None):
     _call("dg_cast_fp8_per_channel", _ptr(x), _ptr(q), _ptr(sf), T, C, _stream(stream))
+
+
+def dg_layer_norm(x, weight, bias, y, q, sfa, mean, rstd, T, K, eps, rms, x_type, w_type, stream=None):
+    _call("dg_layer_norm", _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(q), _ptr(sfa), _ptr(mean), _ptr(rstd), T, K,
+          eps, rms, x_type, w_type, _stream(stream))
+
+
+def dg_layer_norm_backward_workspace(T: int, K: int) -> int:
+    return load().dg_layer_norm_backward_workspace(T, K)
+
+
+def dg_layer_norm_backward(dy, x, weight, mean, rstd, dx, dw, db, workspace, workspace_bytes, T, K, x_type, w_type,
+                           stream=None):
+    _call("dg_layer_norm_backward", _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw), _ptr(db),
+          _ptr(workspace), workspace_bytes, T, K, x_type, w_type, _stream(stream))
+
+
+def dg_moe_route(logits, bias, ids, weights, T, E, k, groups, topk_groups, group_top, score, renorm, scale, dtype,
+                 stream=None):
+    _call("dg_moe_route", _ptr(logits), _ptr(bias), _ptr(ids), _ptr(weights), T, E, k, groups, topk_groups, group_top,
+          score, renorm, scale, dtype, _stream(stream))
+
+
+def dg_moe_route_backward(grad_weights, logits, ids, grad_logits, T, E, k, score, renorm, scale, dtype, stream=None):
+    _call("dg_moe_route_backward", _ptr(grad_weights), _ptr(logits), _ptr(ids), _ptr(grad_logits), T, E, k, score, renorm,
+          scale, dtype, _stream(stream))
+
+
+def dg_moe_layout_workspace(T: int, k: int, G: int) -> int:
+    return load().dg_moe_layout_workspace(T, k, G)
+
+
+def dg_moe_layout_contiguous(ids, dst_rows, grouped_layout, ks, workspace, workspace_bytes, T, k, G, M_sum, stream=None):
+    _call("dg_moe_layout_contiguous", _ptr(ids), _ptr(dst_rows), _ptr(grouped_layout), _ptr(ks), _ptr(workspace),
+          workspace_bytes, T, k, G, M_sum, _stream(stream))
+
+
+def dg_moe_layout_masked(ids, dst_rows, masked_m, workspace, workspace_bytes, T, k, G, M_max, stream=None):
+    _call("dg_moe_layout_masked", _ptr(ids), _ptr(dst_rows), _ptr(masked_m), _ptr(workspace), workspace_bytes, T, k, G,
+          M_max, _stream(stream))
+
+
+def dg_cast_fp8_per_token_scatter_topk(x, dst_rows, q, sfa, T, k, G, M, K, stream=None):
+    _call("dg_cast_fp8_per_token_scatter_topk", _ptr(x), _ptr(dst_rows), _ptr(q), _ptr(sfa), T, k, G, M, K,
+          _stream(stream))
+
+
+def dg_moe_combine(d, dst_rows, weights, c, y, T, k, N, R, stream=None):
+    _call("dg_moe_combine", _ptr(d), _ptr(dst_rows), _ptr(weights), _ptr(c), _ptr(y), T, k, N, R, _stream(stream))
+
+
+def dg_moe_combine_backward(grad_y, d, dst_rows, weights, grouped_layout, grad_d, grad_weights, T, k, N, R, stream=None):
+    _call("dg_moe_combine_backward", _ptr(grad_y), _ptr(d), _ptr(dst_rows), _ptr(weights), _ptr(grouped_layout),
+          _ptr(grad_d), _ptr(grad_weights), T, k, N, R, _stream(stream))
 
 
 def dg_sf_ld(mn: int) -> int:

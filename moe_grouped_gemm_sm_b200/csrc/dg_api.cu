@@ -11,6 +11,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "../../include/dg.h"
@@ -1244,3 +1245,5 @@ const char *dg_status_string(dg_status status) {
 }
 
 }  // extern "C"
+
+#include "dg_block_api.cuh"

@@ -1,0 +1,401 @@
+// dg_block_api.cuh — the C ABI of the operators around the experts' products: argument checks, launch
+// shapes and launches. Part of dg_api.cu (it uses that file's device facts and launch helper).
+#pragma once
+#include "dg_norm.cuh"
+#include "dg_route.cuh"
+#include "dg_rows.cuh"
+
+namespace {
+
+constexpr int kNormMaxK = 32768;
+constexpr int kNormMaxParts = 64;   // row parts of the dw / db sums
+
+bool valid_type(int t) { return t == DG_BF16 || t == DG_FP32; }
+
+// Threads and vectors per thread of a norm kernel: one warp a row, 8 rows a block, for rows of up to
+// 4 vectors a lane; else a block a row. Few rows (fewer than two blocks per SM) spread a row
+// over as many threads as it has vectors; many rows keep 4 vectors in flight per thread.
+struct NormShape {
+    int vpt;
+    dim3 grid, block;
+};
+
+NormShape norm_shape(int T, int nv, int sm_count, int max_threads) {
+    NormShape s;
+    if (nv <= 128) {
+        s.vpt = nv <= 32 ? 1 : (nv <= 64 ? 2 : 4);
+        s.block = dim3(32, 8, 1);
+        s.grid = dim3(static_cast<unsigned>((T + 7) / 8), 1, 1);
+        return s;
+    }
+    s.vpt = T < 2 * sm_count ? 1 : 4;
+    while ((nv + s.vpt - 1) / s.vpt > max_threads) s.vpt *= 2;
+    const int nt = ((nv + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+    s.block = dim3(static_cast<unsigned>(nt), 1, 1);
+    s.grid = dim3(static_cast<unsigned>(T), 1, 1);
+    return s;
+}
+
+// f(vector size, vectors per thread, shape) with the first two as compile-time constants. Rows
+// that are not whole 16-byte vectors go element by element (V = 1). MAXT threads and the K limit
+// bound the vectors per thread at kNormMaxK / (V·MAXT).
+template <typename XT, int MAXT, typename F>
+dg_status norm_dispatch(int T, int K, int sm_count, F f) {
+    constexpr int V = 16 / static_cast<int>(sizeof(XT)), TOP = kNormMaxK / (V * MAXT);
+    using std::integral_constant;
+    if (K % V == 0) {
+        const NormShape s = norm_shape(T, K / V, sm_count, MAXT);
+        if (s.vpt == 1) return f(integral_constant<int, V>(), integral_constant<int, 1>(), s);
+        if (s.vpt == 2) return f(integral_constant<int, V>(), integral_constant<int, 2>(), s);
+        if (s.vpt == 4) return f(integral_constant<int, V>(), integral_constant<int, 4>(), s);
+        if constexpr (TOP >= 8)
+            if (s.vpt == 8) return f(integral_constant<int, V>(), integral_constant<int, 8>(), s);
+        if constexpr (TOP >= 16)
+            if (s.vpt == 16) return f(integral_constant<int, V>(), integral_constant<int, 16>(), s);
+        return DG_ERR_INVALID_ARG;
+    }
+    const NormShape s = norm_shape(T, K, sm_count, MAXT);
+    if (s.vpt <= 4) return f(integral_constant<int, 1>(), integral_constant<int, 4>(), s);
+    return f(integral_constant<int, 1>(), integral_constant<int, TOP * V>(), s);
+}
+
+template <typename XT, typename WT>
+dg_status run_layer_norm(const dg::NormParams &p, int sm_count, cudaStream_t st) {
+    return norm_dispatch<XT, dg::NORM_MAX_THREADS>(p.T, p.K, sm_count, [&](auto v, auto vpt, const NormShape &s) {
+        Launch ln(s.grid, s.block, 0, st);
+        return from_cuda(cudaLaunchKernelEx(
+            &ln.cfg, dg::layer_norm_kernel<XT, WT, decltype(v)::value, decltype(vpt)::value>, p));
+    });
+}
+
+template <typename XT, typename WT>
+dg_status run_layer_norm_backward(const dg::NormBackParams &p, int sm_count, cudaStream_t st) {
+    dg_status s =
+        norm_dispatch<XT, dg::NORM_DX_MAX_THREADS>(p.T, p.K, sm_count, [&](auto v, auto vpt, const NormShape &sh) {
+            Launch ln(sh.grid, sh.block, 0, st);
+            return from_cuda(cudaLaunchKernelEx(
+                &ln.cfg, dg::layer_norm_dx_kernel<XT, WT, decltype(v)::value, decltype(vpt)::value>, p));
+        });
+    if (s != DG_OK || (!p.dw && !p.db)) return s;
+    {
+        Launch ln(dim3(static_cast<unsigned>((p.K + 31) / 32), static_cast<unsigned>(p.parts), 1), dim3(32, 8, 1), 0, st);
+        s = from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::layer_norm_dwdb_kernel<XT>, p));
+        if (s != DG_OK) return s;
+    }
+    Launch ln(dim3(static_cast<unsigned>((p.K + 255) / 256), 1, 1), dim3(256, 1, 1), 0, st);
+    return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::layer_norm_parts_kernel, p));
+}
+
+int norm_parts(int T) { return std::max(1, std::min(kNormMaxParts, (T + 7) / 8)); }
+
+// Argument checks that both directions of the routing share.
+dg_status check_route(int T, int E, int k, int score, int dtype) {
+    if (T < 0 || E <= 0 || E > dg::ROUTE_MAX_E || k <= 0 || k > dg::ROUTE_MAX_K || k > E || !valid_type(dtype) ||
+        (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID))
+        return DG_ERR_INVALID_ARG;
+    return DG_OK;
+}
+
+template <typename LT>
+dg_status run_route(const dg::RouteParams &p, cudaStream_t st) {
+    Launch ln(dim3(static_cast<unsigned>((p.T + dg::ROUTE_WARPS - 1) / dg::ROUTE_WARPS), 1, 1),
+              dim3(32 * dg::ROUTE_WARPS, 1, 1), 0, st);
+    const int per_lane = (p.E + 31) / 32;
+    if (per_lane <= 1) return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::route_kernel<LT, 1>, p));
+    if (per_lane <= 2) return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::route_kernel<LT, 2>, p));
+    if (per_lane <= 4) return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::route_kernel<LT, 4>, p));
+    if (per_lane <= 8) return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::route_kernel<LT, 8>, p));
+    if (per_lane <= 16) return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::route_kernel<LT, 16>, p));
+    return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::route_kernel<LT, 32>, p));
+}
+
+// Pairs per block of the layout kernels, a multiple of 256.
+int layout_chunk(int n) {
+    if (n <= dg::LAYOUT_CHUNK) return dg::LAYOUT_CHUNK;
+    const int c = (n + dg::LAYOUT_MAX_CHUNKS - 1) / dg::LAYOUT_MAX_CHUNKS;
+    return std::max(dg::LAYOUT_CHUNK, (c + 255) / 256 * 256);
+}
+
+bool layout_sizes_ok(int T, int k, int G) {
+    return T >= 0 && k > 0 && G > 0 && G <= dg::LAYOUT_MAX_G && static_cast<long long>(T) * k <= (1LL << 30);
+}
+
+template <bool MASKED>
+dg_status run_layout(const int32_t *ids, int32_t *dst_rows, int32_t *grouped_layout, int32_t *counts, void *workspace,
+                     long long workspace_bytes, int T, int k, int G, int M, cudaStream_t st) {
+    const long long need = dg_moe_layout_workspace(T, k, G);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return DG_ERR_INVALID_ARG;
+    const DeviceInfo *di = nullptr;
+    dg_status s = device_info(&di);
+    if (s != DG_OK) return s;
+    dg::LayoutParams p{};
+    p.ids = ids;
+    p.dst_rows = dst_rows;
+    p.grouped_layout = grouped_layout;
+    p.counts = counts;
+    p.hist = static_cast<int32_t *>(workspace);
+    p.err = di->err;
+    p.n = T * k;
+    p.G = G;
+    p.M = M;
+    p.chunk = layout_chunk(p.n);
+    p.chunks = std::max(1, static_cast<int>((static_cast<long long>(p.n) + p.chunk - 1) / p.chunk));
+    const dim3 grid(static_cast<unsigned>(p.chunks), 1, 1), block(dg::LAYOUT_THREADS, 1, 1);
+    if (p.chunks > 1) {
+        Launch ln(grid, block, static_cast<size_t>(G) * 4, st);
+        s = from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::layout_count_kernel, p));
+        if (s != DG_OK) return s;
+    }
+    Launch ln(grid, block, static_cast<size_t>(G) * 4 * (2 + dg::LAYOUT_WARPS), st);
+    return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::layout_place_kernel<MASKED>, p));
+}
+
+}  // namespace
+
+extern "C" {
+
+dg_status dg_layer_norm(const void *x, const void *weight, const void *bias, void *y, void *q, float *sfa, float *mean,
+                        float *rstd, int T, int K, float eps, int rms, int x_type, int w_type, void *stream) {
+    if (!x || (!y && !q) || (q != nullptr) != (sfa != nullptr) || T < 0 || K <= 0 || K > kNormMaxK || !(eps >= 0.f) ||
+        !valid_type(x_type) || !valid_type(w_type) || (rms && bias) || (q && K % 128 != 0))
+        return DG_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(weight) || !aligned16(bias) || !aligned16(y) || !aligned16(q) || !aligned16(sfa))
+        return DG_ERR_ALIGNMENT;
+    if (T == 0) return DG_OK;
+    const DeviceInfo *di = nullptr;
+    dg_status s = device_info(&di);
+    if (s != DG_OK) return s;
+    dg::NormParams p{};
+    p.x = x;
+    p.w = weight;
+    p.b = bias;
+    p.y = y;
+    p.q = static_cast<uint8_t *>(q);
+    p.sfa = sfa;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.T = T;
+    p.K = K;
+    p.ld = pad4(T);
+    p.rms = rms ? 1 : 0;
+    p.eps = eps;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (x_type == DG_BF16)
+        return w_type == DG_BF16 ? run_layer_norm<__nv_bfloat16, __nv_bfloat16>(p, di->sm_count, st)
+                                 : run_layer_norm<__nv_bfloat16, float>(p, di->sm_count, st);
+    return w_type == DG_BF16 ? run_layer_norm<float, __nv_bfloat16>(p, di->sm_count, st)
+                             : run_layer_norm<float, float>(p, di->sm_count, st);
+}
+
+long long dg_layer_norm_backward_workspace(int T, int K) {
+    if (T <= 0 || K <= 0 || K > kNormMaxK) return 0;
+    return static_cast<long long>(norm_parts(T)) * 2 * K * 4;
+}
+
+dg_status dg_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean, const float *rstd,
+                                 void *dx, float *dw, float *db, void *workspace, long long workspace_bytes, int T, int K,
+                                 int x_type, int w_type, void *stream) {
+    if (!dy || !x || !rstd || !dx || T < 0 || K <= 0 || K > kNormMaxK || !valid_type(x_type) || !valid_type(w_type))
+        return DG_ERR_INVALID_ARG;
+    if ((dw || db) && T > 0 && (!workspace || workspace_bytes < dg_layer_norm_backward_workspace(T, K)))
+        return DG_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(weight) || !aligned16(dx) || !aligned16(dw) || !aligned16(db) ||
+        !aligned16(workspace))
+        return DG_ERR_ALIGNMENT;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {   // sums over no rows
+        if ((dw && cudaMemsetAsync(dw, 0, static_cast<size_t>(K) * 4, st) != cudaSuccess) ||
+            (db && cudaMemsetAsync(db, 0, static_cast<size_t>(K) * 4, st) != cudaSuccess))
+            return DG_ERR_CUDA;
+        return DG_OK;
+    }
+    const DeviceInfo *di = nullptr;
+    dg_status s = device_info(&di);
+    if (s != DG_OK) return s;
+    dg::NormBackParams p{};
+    p.dy = dy;
+    p.x = x;
+    p.w = weight;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.dx = dx;
+    p.part = static_cast<float *>(workspace);
+    p.dw = dw;
+    p.db = db;
+    p.T = T;
+    p.K = K;
+    p.parts = norm_parts(T);
+    if (x_type == DG_BF16)
+        return w_type == DG_BF16 ? run_layer_norm_backward<__nv_bfloat16, __nv_bfloat16>(p, di->sm_count, st)
+                                 : run_layer_norm_backward<__nv_bfloat16, float>(p, di->sm_count, st);
+    return w_type == DG_BF16 ? run_layer_norm_backward<float, __nv_bfloat16>(p, di->sm_count, st)
+                             : run_layer_norm_backward<float, float>(p, di->sm_count, st);
+}
+
+dg_status dg_moe_route(const void *logits, const float *bias, int32_t *ids, float *weights, int T, int E, int k,
+                       int groups, int topk_groups, int group_top, int score, int renorm, float scale, int dtype,
+                       void *stream) {
+    if (!logits || !ids || !weights) return DG_ERR_INVALID_ARG;
+    dg_status s = check_route(T, E, k, score, dtype);
+    if (s != DG_OK) return s;
+    if (groups <= 0 || groups > dg::ROUTE_MAX_GROUPS || E % groups != 0 || topk_groups <= 0 || topk_groups > groups ||
+        group_top < 1 || group_top > 2 || !(scale - scale == 0.f))
+        return DG_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned16(bias) || !aligned16(ids) || !aligned16(weights)) return DG_ERR_ALIGNMENT;
+    if (T == 0) return DG_OK;
+    const DeviceInfo *di = nullptr;
+    s = device_info(&di);
+    if (s != DG_OK) return s;
+    dg::RouteParams p{};
+    p.logits = logits;
+    p.bias = bias;
+    p.ids = ids;
+    p.weights = weights;
+    p.err = di->err;
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.groups = topk_groups == groups ? 1 : groups;   // every group kept: no choice between groups
+    p.topk_groups = topk_groups;
+    p.group_top = group_top;
+    p.score = score;
+    p.renorm = renorm ? 1 : 0;
+    p.scale = scale;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dtype == DG_BF16 ? run_route<__nv_bfloat16>(p, st) : run_route<float>(p, st);
+}
+
+dg_status dg_moe_route_backward(const float *grad_weights, const void *logits, const int32_t *ids, void *grad_logits,
+                                int T, int E, int k, int score, int renorm, float scale, int dtype, void *stream) {
+    if (!grad_weights || !logits || !ids || !grad_logits || !(scale - scale == 0.f)) return DG_ERR_INVALID_ARG;
+    dg_status s = check_route(T, E, k, score, dtype);
+    if (s != DG_OK) return s;
+    if (!aligned16(grad_weights) || !aligned16(logits) || !aligned16(ids) || !aligned16(grad_logits))
+        return DG_ERR_ALIGNMENT;
+    if (T == 0) return DG_OK;
+    const DeviceInfo *di = nullptr;
+    s = device_info(&di);
+    if (s != DG_OK) return s;
+    dg::RouteParams p{};
+    p.logits = logits;
+    p.ids = const_cast<int32_t *>(ids);
+    p.grad_w = grad_weights;
+    p.grad_logits = grad_logits;
+    p.err = di->err;
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.score = score;
+    p.renorm = renorm ? 1 : 0;
+    p.scale = scale;
+    Launch ln(dim3(static_cast<unsigned>((T + dg::ROUTE_WARPS - 1) / dg::ROUTE_WARPS), 1, 1),
+              dim3(32 * dg::ROUTE_WARPS, 1, 1), 0, static_cast<cudaStream_t>(stream));
+    return from_cuda(dtype == DG_BF16 ? cudaLaunchKernelEx(&ln.cfg, dg::route_backward_kernel<__nv_bfloat16>, p)
+                                      : cudaLaunchKernelEx(&ln.cfg, dg::route_backward_kernel<float>, p));
+}
+
+long long dg_moe_layout_workspace(int T, int k, int G) {
+    if (!layout_sizes_ok(T, k, G)) return 0;
+    const int n = T * k, chunk = layout_chunk(n);
+    const long long chunks = (static_cast<long long>(n) + chunk - 1) / chunk;
+    return chunks > 1 ? chunks * G * 4 : 0;
+}
+
+dg_status dg_moe_layout_contiguous(const int32_t *ids, int32_t *dst_rows, int32_t *grouped_layout, int32_t *ks,
+                                   void *workspace, long long workspace_bytes, int T, int k, int G, int M_sum,
+                                   void *stream) {
+    if ((T > 0 && (!ids || !dst_rows)) || (M_sum > 0 && !grouped_layout) || !layout_sizes_ok(T, k, G) || M_sum < 0 || M_sum % 128 != 0)
+        return DG_ERR_INVALID_ARG;
+    if (!aligned16(ids) || !aligned16(dst_rows) || !aligned16(grouped_layout) || !aligned16(ks) || !aligned16(workspace))
+        return DG_ERR_ALIGNMENT;
+    return run_layout<false>(ids, dst_rows, grouped_layout, ks, workspace, workspace_bytes, T, k, G, M_sum,
+                             static_cast<cudaStream_t>(stream));
+}
+
+dg_status dg_moe_layout_masked(const int32_t *ids, int32_t *dst_rows, int32_t *masked_m, void *workspace,
+                               long long workspace_bytes, int T, int k, int G, int M_max, void *stream) {
+    if ((T > 0 && (!ids || !dst_rows)) || !masked_m || !layout_sizes_ok(T, k, G) || M_max < 0 ||
+        static_cast<long long>(G) * M_max >= (1LL << 31))
+        return DG_ERR_INVALID_ARG;
+    if (!aligned16(ids) || !aligned16(dst_rows) || !aligned16(masked_m) || !aligned16(workspace)) return DG_ERR_ALIGNMENT;
+    return run_layout<true>(ids, dst_rows, nullptr, masked_m, workspace, workspace_bytes, T, k, G, M_max,
+                            static_cast<cudaStream_t>(stream));
+}
+
+dg_status dg_cast_fp8_per_token_scatter_topk(const void *x, const int32_t *dst_rows, void *q, float *sfa, int T, int k,
+                                             int G, int M, int K, void *stream) {
+    if (!x || !dst_rows || !q || !sfa || T < 0 || k <= 0 || G <= 0 || M < 0 || K <= 0 || K % 128 != 0 ||
+        static_cast<long long>(G) * M >= (1LL << 31) || static_cast<long long>(T) * k > (1LL << 30))
+        return DG_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(sfa)) return DG_ERR_ALIGNMENT;
+    if (T == 0 || M == 0) return DG_OK;
+    const DeviceInfo *di = nullptr;
+    dg_status s = device_info(&di);
+    if (s != DG_OK) return s;
+    const long long blocks = (static_cast<long long>(T) * (K / 128) + 15) / 16;
+    if (blocks >= (1LL << 31)) return DG_ERR_INVALID_ARG;
+    Launch ln(dim3(static_cast<unsigned>(blocks), 1, 1), dim3(256, 1, 1), 0, static_cast<cudaStream_t>(stream));
+    return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::cast_scatter_topk_kernel, static_cast<const __nv_bfloat16 *>(x),
+                                        dst_rows, static_cast<uint8_t *>(q), sfa, T, k, K, M, pad4(M),
+                                        static_cast<long long>(G) * M, di->err));
+}
+
+dg_status dg_moe_combine(const void *d, const int32_t *dst_rows, const float *weights, const void *c, void *y, int T,
+                         int k, int N, int R, void *stream) {
+    if ((R > 0 && !d) || (T > 0 && (!dst_rows || !y)) || T < 0 || k <= 0 || k > dg::COMBINE_MAX_K || N <= 0 || N % 8 != 0 || R < 0)
+        return DG_ERR_INVALID_ARG;
+    if (!aligned16(d) || !aligned16(c) || !aligned16(y)) return DG_ERR_ALIGNMENT;
+    if (T == 0) return DG_OK;
+    const DeviceInfo *di = nullptr;
+    dg_status s = device_info(&di);
+    if (s != DG_OK) return s;
+    dg::CombineParams p{};
+    p.d = static_cast<const __nv_bfloat16 *>(d);
+    p.dst = dst_rows;
+    p.w = weights;
+    p.c = static_cast<const __nv_bfloat16 *>(c);
+    p.y = static_cast<__nv_bfloat16 *>(y);
+    p.err = di->err;
+    p.T = T;
+    p.k = k;
+    p.N = N;
+    p.R = R;
+    const unsigned parts = static_cast<unsigned>(std::min(65535, (N / 8 + dg::COMBINE_THREADS - 1) / dg::COMBINE_THREADS));
+    Launch ln(dim3(static_cast<unsigned>(T), parts, 1), dim3(dg::COMBINE_THREADS, 1, 1), 0,
+              static_cast<cudaStream_t>(stream));
+    return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::combine_kernel, p));
+}
+
+dg_status dg_moe_combine_backward(const void *grad_y, const void *d, const int32_t *dst_rows, const float *weights,
+                                  const int32_t *grouped_layout, void *grad_d, float *grad_weights, int T, int k, int N,
+                                  int R, void *stream) {
+    if ((T > 0 && (!grad_y || !dst_rows)) || (T > 0 && R > 0 && !grad_d && !grad_weights) ||
+        (R > 0 && grad_weights && !d) || (grouped_layout && !grad_d) || T < 0 || k <= 0 || k > dg::COMBINE_MAX_K || N <= 0 || N % 8 != 0 || R < 0)
+        return DG_ERR_INVALID_ARG;
+    if (!aligned16(grad_y) || !aligned16(d) || !aligned16(grad_d)) return DG_ERR_ALIGNMENT;
+    const DeviceInfo *di = nullptr;
+    dg_status s = device_info(&di);
+    if (s != DG_OK) return s;
+    dg::CombineParams p{};
+    p.d = static_cast<const __nv_bfloat16 *>(d);
+    p.dst = dst_rows;
+    p.w = weights;
+    p.gy = static_cast<const __nv_bfloat16 *>(grad_y);
+    p.layout = grouped_layout;
+    p.gd = static_cast<__nv_bfloat16 *>(grad_d);
+    p.gw = grad_weights;
+    p.err = di->err;
+    p.T = T;
+    p.k = k;
+    p.N = N;
+    p.R = R;
+    const long long zero_blocks = grouped_layout ? std::min(R, 8 * di->sm_count) : 0;
+    const long long blocks = T + zero_blocks;
+    if (blocks == 0) return DG_OK;
+    if (blocks >= (1LL << 31)) return DG_ERR_INVALID_ARG;
+    Launch ln(dim3(static_cast<unsigned>(blocks), 1, 1), dim3(dg::COMBINE_THREADS, 1, 1), 0,
+              static_cast<cudaStream_t>(stream));
+    return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::combine_backward_kernel, p));
+}
+
+}  // extern "C"

@@ -81,6 +81,18 @@ __device__ __forceinline__ uint2 quant8(const float (&f)[8], float s) {
     return make_uint2(w[0], w[1]);
 }
 
+// 4 values -> 4 e4m3 codes, by the same rule.
+__device__ __forceinline__ uint32_t quant4(const float (&f)[4], float s) {
+    uint32_t acc = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 pr = make_float2(__fdiv_rn(f[2 * i], s), __fdiv_rn(f[2 * i + 1], s));
+        const uint32_t two = __nv_cvt_float2_to_fp8x2(pr, __NV_SATFINITE, __NV_E4M3);
+        acc |= (two & 0xFFFFu) << (16 * i);
+    }
+    return acc;
+}
+
 // Per-token cast. Block: 256 threads covering ROWS rows x KBS K-slices of one batch entry, in
 // "slice halves": a half-warp covers one row's 128-value slice (16 lanes x 8 values, 16 bytes
 // per lane). Slice s = i·16 + warp·2 + half (i < ROWS·KBS/16) is row s / KBS, slice s % KBS, so

@@ -1,0 +1,234 @@
+"""Layer norm and RMS norm (forward, FP8 cast epilogue, backward) against their formulas in 64 bits.
+
+Tolerances count roundings. u = 2^-24 is half a step of fp32. A sum of K terms is taken as at
+most 32 (a thread) + 5 (its warp) + 32 (the warps) additions one after another, so a mean is
+within 72u of the mean of the magnitudes; every other step adds a few u. With 80u for all of
+them: |dy| <= 80u·(|xh·w| + r·|w|·mean|x| + |b|), and half a step of the output type on top."""
+import numpy as np
+import pytest
+import torch
+
+from moe_grouped_gemm_sm_b200 import _lib, build, ops
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+def make(T, K, xt, wt, rms, seed=0, weight=True, bias=True):
+    g = torch.Generator().manual_seed(seed * 7919 + T * 31 + K)
+    x = (torch.randn(T, K, generator=g) * (0.3 + torch.rand(T, 1, generator=g) * 3) + 0.4).to(xt)
+    if K > 5:
+        x[:, 5] *= 20
+    w = (1 + 0.3 * torch.randn(K, generator=g)).to(wt) if weight else None
+    b = (0.5 * torch.randn(K, generator=g)).to(wt) if bias and not rms else None
+    return x, w, b
+
+
+def ref_forward(x, w, b, eps, rms):
+    x = x.double()
+    mu = torch.zeros(x.shape[0], 1, dtype=torch.float64) if rms else x.mean(1, keepdim=True)
+    r = 1 / ((x - mu).square().mean(1, keepdim=True) + eps).sqrt()
+    xh = (x - mu) * r
+    w = torch.ones(x.shape[1], dtype=torch.float64) if w is None else w.double()
+    b = torch.zeros(x.shape[1], dtype=torch.float64) if b is None else b.double()
+    tol = 80 * U * ((xh * w).abs() + r * w.abs() * x.abs().mean(1, keepdim=True) + b.abs())
+    return xh * w + b, mu[:, 0], r[:, 0], tol
+
+
+def cuda(t):
+    return None if t is None else t.cuda()
+
+
+SHAPES = [(1, 1), (3, 2), (2, 7), (9, 64), (5, 129), (17, 1000), (300, 1001), (1, 7168), (33, 2048), (311, 7168),
+          (7, 4097), (2, 8191), (600, 24), (3, 16384), (2, 20001), (2, 32768), (299, 260)]
+
+
+@pytest.mark.parametrize("T,K", SHAPES)
+@pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rms", [False, True])
+def test_forward(T, K, xt, rms):
+    for wt, weight, bias in ((torch.float32, True, True), (torch.bfloat16, True, False), (torch.bfloat16, False, True)):
+        x, w, b = make(T, K, xt, wt, rms, weight=weight, bias=bias)
+        y, mean, rstd = ops.layer_norm(cuda(x), cuda(w), cuda(b), eps=1e-5, rms=rms, stats=True)
+        ref, mu, r, tol = ref_forward(x, w, b, 1e-5, rms)
+        assert y.dtype == xt and ((y.cpu().double() - ref).abs() <= tol + STEP[xt] * (ref.abs() + tol)).all()
+        # r: the mean square within 80u and twice the mean's error over the deviation
+        mabs = x.double().abs().mean(1)
+        assert ((rstd.cpu().double() - r).abs() <= 80 * U * r * (1 + r * mabs)).all()
+        if rms:
+            assert mean is None
+        else:
+            assert ((mean.cpu().double() - mu).abs() <= 80 * U * mabs).all()
+
+
+def test_forward_in_place_and_no_rows():
+    x, w, b = make(70, 520, torch.bfloat16, torch.float32, False)
+    ref = ops.layer_norm(cuda(x), cuda(w), cuda(b))
+    xd = cuda(x)
+    assert ops.layer_norm(xd, cuda(w), cuda(b), out=xd) is xd and torch.equal(xd, ref)
+    e = torch.empty(0, 64, device="cuda")
+    assert ops.layer_norm(e).shape == (0, 64)
+    dx, dw, db = ops.layer_norm_backward(e, e, torch.ones(64, device="cuda"), e[:, 0], e[:, 0])
+    assert dx.shape == (0, 64) and not dw.any() and not db.any()
+
+
+def test_constant_rows_and_large_offsets():
+    """A constant row has deviation 0 (r = 1/sqrt(eps)); a large mean must not eat the deviation."""
+    x = torch.full((4, 768), 3.0)
+    x[1] = 0
+    x[2] = 1000 + torch.linspace(-1, 1, 768)
+    x[3] = -5e4
+    y = ops.layer_norm(x.cuda(), eps=1e-5).cpu().double()
+    ref, _, _, tol = ref_forward(x, None, None, 1e-5, False)
+    assert ((y - ref).abs() <= tol + U).all()
+    y = ops.layer_norm(x.cuda(), eps=1e-5, rms=True).cpu().double()
+    ref, _, _, tol = ref_forward(x, None, None, 1e-5, True)
+    assert ((y - ref).abs() <= tol + U).all()
+
+
+@pytest.mark.parametrize("T,K", [(1, 128), (5, 256), (6, 1024), (16, 7168), (301, 7168), (1000, 128), (3, 20480), (303, 1152)])
+@pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rms", [False, True])
+def test_cast(T, K, xt, rms):
+    x, w, b = make(T, K, xt, torch.bfloat16, rms, seed=2)
+    q, sfa = ops.layer_norm_cast(cuda(x), cuda(w), cuda(b), rms=rms)
+    ref, _, _, tol = ref_forward(x, w, b, 1e-5, rms)
+    code = q.cpu().view(torch.float8_e4m3fn).double().view(T, K // 128, 128)
+    s = sfa.cpu()[:, :T].t().double()
+    assert not sfa.cpu()[:, T:].any()
+    cells, ctol = ref.view(T, -1, 128), tol.view(T, -1, 128)
+    amax, atol = cells.abs().amax(2), ctol.amax(2)
+    assert ((s - amax / 448).abs() <= (atol + 2 * U * amax) / 448).all()
+    # a code is within half a step of the value it stands for: 2^-4 of it, or 2^-10 among the subnormals
+    err = (code * s.unsqueeze(2) - cells).abs()
+    bound = torch.maximum(2.0 ** -4 * (cells.abs() + ctol), 2.0 ** -10 * s.unsqueeze(2)) + ctol + 4 * U * cells.abs()
+    assert (err <= bound).all()
+    if xt == torch.float32:   # the fp32 result is not rounded before the cast: the same scales and codes
+        y = ops.layer_norm(cuda(x), cuda(w), cuda(b), rms=rms).cpu().view(T, -1, 128)
+        sc = y.abs().amax(2) / 448
+        assert torch.equal(sc, sfa.cpu()[:, :T].t())
+        assert torch.equal((y / sc.unsqueeze(2)).view(T, K).to(torch.float8_e4m3fn).view(torch.uint8), q.cpu())
+
+
+def test_cast_of_zero_rows():
+    q, sfa = ops.layer_norm_cast(torch.zeros(3, 256, dtype=torch.bfloat16, device="cuda"))
+    assert not q.any() and (sfa[:, :3] == 1).all()
+
+
+def ref_backward(dy, x, w, mean, rstd, rms):
+    """Gradients from the fp32 statistics, and their tolerances."""
+    dy, x = dy.double(), x.double()
+    mu = 0 if rms else mean.double()[:, None]
+    r = rstd.double()[:, None]
+    w = torch.ones(x.shape[1], dtype=torch.float64) if w is None else w.double()
+    xh, uu = (x - mu) * r, dy * w
+    c1 = 0 if rms else uu.mean(1, keepdim=True)
+    c2 = (uu * xh).mean(1, keepdim=True)
+    dx = r * (uu - c1 - xh * c2)
+    a1, a2 = uu.abs().mean(1, keepdim=True), (uu * xh).abs().mean(1, keepdim=True)
+    tol = 80 * U * r * (uu.abs() + (0 if rms else a1) + xh.abs() * a2)
+    # a column's sum over T rows: at most T - 1 additions one after another, 8 roundings a term
+    return dx, tol, (dy * xh).sum(0), (x.shape[0] + 8) * U * (dy * xh).abs().sum(0), dy.sum(0), \
+        (x.shape[0] + 8) * U * dy.abs().sum(0)
+
+
+@pytest.mark.parametrize("T,K", SHAPES + [(2000, 512), (1111, 7168), (5000, 40), (4000, 33)])
+@pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rms", [False, True])
+def test_backward(T, K, xt, rms):
+    for wt, weight, bias in ((torch.float32, True, True), (torch.bfloat16, True, False), (torch.bfloat16, False, True)):
+        x, w, _ = make(T, K, xt, wt, rms, seed=3, weight=weight)
+        dy = torch.randn(T, K, generator=torch.Generator().manual_seed(T + K)).to(xt)
+        _, mu, r, _ = ref_forward(x, w, None, 1e-5, rms)
+        mean, rstd = None if rms else mu.float(), r.float()
+        dx, dw, db = ops.layer_norm_backward(cuda(dy), cuda(x), cuda(w), cuda(mean), cuda(rstd), bias=bias and not rms,
+                                             rms=rms)
+        rx, tx, rw, tw, rb, tb = ref_backward(dy, x, w, mean, rstd, rms)
+        assert dx.dtype == xt and ((dx.cpu().double() - rx).abs() <= tx + STEP[xt] * (rx.abs() + tx)).all()
+        assert (dw is not None) == weight and (db is not None) == (bias and not rms)
+        if weight:
+            assert ((dw.cpu().double() - rw).abs() <= tw).all()
+        if db is not None:
+            assert ((db.cpu().double() - rb).abs() <= tb).all()
+
+
+@pytest.mark.parametrize("rms", [False, True])
+def test_backward_against_differences(rms):
+    """The directional derivative of sum(y·dy) along v, from the kernels' gradients and from central
+    differences of the 64-bit forward. The second carries an error of h^2; the first one the
+    tolerances above, summed over the elements."""
+    T, K, h = 6, 96, 1e-5
+    x, w, b = make(T, K, torch.float32, torch.float32, rms, seed=4)
+    g = torch.Generator().manual_seed(5)
+    dy, vx, vw, vb = (torch.randn(s, generator=g) for s in ((T, K), (T, K), (K,), (K,)))
+    _, mean, rstd = ops.layer_norm(cuda(x), cuda(w), cuda(b), rms=rms, stats=True)
+    dx, dw, db = ops.layer_norm_backward(cuda(dy), cuda(x), cuda(w), mean, rstd, bias=not rms, rms=rms)
+
+    def f(s):
+        bb = None if rms else b.double() + s * vb.double()
+        y = ref_forward(x.double() + s * vx.double(), w.double() + s * vw.double(), bb, 1e-5, rms)[0]
+        return float((y * dy.double()).sum())
+    num = (f(h) - f(-h)) / (2 * h)
+    got = float((dx.cpu().double() * vx).sum() + (dw.cpu().double() * vw).sum())
+    if not rms:
+        got += float((db.cpu().double() * vb).sum())
+    rx, tx, _, tw, _, tb = ref_backward(dy, x, w, None if rms else mean.cpu(), rstd.cpu(), rms)
+    # the statistics' own error (80u of r, twice over in the products) moves dx by as much again
+    allow = float((3 * tx * vx.abs()).sum() + (3 * tw * vw.abs()).sum() + (tb * vb.abs()).sum())
+    curve = 1e-6 * abs(num) + 1e-6   # h^2 = 1e-10 times third derivatives, and 1e-16/h of the differences
+    assert abs(got - num) <= allow + curve
+
+
+def test_same_bits_every_time_on_streams_and_in_graphs():
+    x, w, b = make(700, 1536, torch.bfloat16, torch.float32, False, seed=6)
+    dy = torch.randn(700, 1536, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    x, w, b, dy = (t.cuda() for t in (x, w, b, dy))
+
+    def step(stream=None):
+        y, mean, rstd = ops.layer_norm(x, w, b, stats=True, stream=stream)
+        return (y, *ops.layer_norm_backward(dy, x, w, mean, rstd, stream=stream), *ops.layer_norm_cast(x, w, b, stream=stream))
+    ref = step()
+    torch.cuda.synchronize()
+    for s in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        got = step(s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, ref))
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, out))
+    for graph, out in graphs + graphs:
+        for o in out:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, ref))
+
+
+def test_refusals():
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(256, device="cuda")
+    s = torch.zeros(4, device="cuda")
+    for call in (lambda: ops.layer_norm(x.t()), lambda: ops.layer_norm(x.half()), lambda: ops.layer_norm(x[0]),
+                 lambda: ops.layer_norm(x, w[:128]), lambda: ops.layer_norm(x, w.double()), lambda: ops.layer_norm(x, w, rms=True, bias=w),
+                 lambda: ops.layer_norm(x, w, w.bfloat16()), lambda: ops.layer_norm(x, out=x.float()),
+                 lambda: ops.layer_norm_cast(x[:, :200].contiguous()), lambda: ops.layer_norm_backward(x.float(), x, w, s, s),
+                 lambda: ops.layer_norm_backward(x, x, w, None, s), lambda: ops.layer_norm_backward(x, x, w, s, s[:2]),
+                 lambda: ops.layer_norm_backward(x, x, w, None, s, rms=True, bias=True)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(_lib.DgError):
+        ops.layer_norm(torch.zeros(1, 40000, device="cuda"))
+    with pytest.raises(_lib.DgError):
+        ops.layer_norm(x, eps=-1.0)
+    with pytest.raises(_lib.DgError) as e:
+        ops.layer_norm(torch.zeros(4 * 64 + 8, dtype=torch.bfloat16, device="cuda")[4:260].view(4, 64))
+    assert e.value.status == _lib.DG_ERR_ALIGNMENT
