@@ -10,6 +10,8 @@ namespace {
 constexpr int kNormMaxK = 32768;
 constexpr int kNormMaxParts = 64;   // row parts of the dw / db sums
 
+constexpr int kMaxRows = 1 << 30;
+
 bool valid_type(int t) { return t == DG_BF16 || t == DG_FP32; }
 
 // Threads and vectors per thread of a norm kernel: one warp a row, 8 rows a block, for rows of up to
@@ -90,16 +92,17 @@ int norm_parts(int T) { return std::max(1, std::min(kNormMaxParts, (T + 7) / 8))
 
 // Argument checks that both directions of the routing share.
 dg_status check_route(int T, int E, int k, int score, int dtype) {
-    if (T < 0 || E <= 0 || E > dg::ROUTE_MAX_E || k <= 0 || k > dg::ROUTE_MAX_K || k > E || !valid_type(dtype) ||
+    if (T < 0 || T > kMaxRows || E <= 0 || E > dg::ROUTE_MAX_E || k <= 0 || k > dg::ROUTE_MAX_K || k > E || !valid_type(dtype) ||
         (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID))
         return DG_ERR_INVALID_ARG;
     return DG_OK;
 }
 
+// A warp takes a token; warps beyond 32 an SM take further ones (they keep the bias in registers).
 template <typename LT>
-dg_status run_route(const dg::RouteParams &p, cudaStream_t st) {
-    Launch ln(dim3(static_cast<unsigned>((p.T + dg::ROUTE_WARPS - 1) / dg::ROUTE_WARPS), 1, 1),
-              dim3(32 * dg::ROUTE_WARPS, 1, 1), 0, st);
+dg_status run_route(const dg::RouteParams &p, int sm_count, cudaStream_t st) {
+    const int blocks = std::min((p.T + dg::ROUTE_WARPS - 1) / dg::ROUTE_WARPS, sm_count * 32 / dg::ROUTE_WARPS);
+    Launch ln(dim3(static_cast<unsigned>(blocks), 1, 1), dim3(32 * dg::ROUTE_WARPS, 1, 1), 0, st);
     const int per_lane = (p.E + 31) / 32;
     if (per_lane <= 1) return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::route_kernel<LT, 1>, p));
     if (per_lane <= 2) return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::route_kernel<LT, 2>, p));
@@ -156,7 +159,7 @@ extern "C" {
 
 dg_status dg_layer_norm(const void *x, const void *weight, const void *bias, void *y, void *q, float *sfa, float *mean,
                         float *rstd, int T, int K, float eps, int rms, int x_type, int w_type, void *stream) {
-    if (!x || (!y && !q) || (q != nullptr) != (sfa != nullptr) || T < 0 || K <= 0 || K > kNormMaxK || !(eps >= 0.f) ||
+    if (!x || (!y && !q) || (q != nullptr) != (sfa != nullptr) || T < 0 || T > kMaxRows || K <= 0 || K > kNormMaxK || !(eps >= 0.f) ||
         !valid_type(x_type) || !valid_type(w_type) || (rms && bias) || (q && K % 128 != 0))
         return DG_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(weight) || !aligned16(bias) || !aligned16(y) || !aligned16(q) || !aligned16(sfa))
@@ -195,7 +198,7 @@ long long dg_layer_norm_backward_workspace(int T, int K) {
 dg_status dg_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean, const float *rstd,
                                  void *dx, float *dw, float *db, void *workspace, long long workspace_bytes, int T, int K,
                                  int x_type, int w_type, void *stream) {
-    if (!dy || !x || !rstd || !dx || T < 0 || K <= 0 || K > kNormMaxK || !valid_type(x_type) || !valid_type(w_type))
+    if (!dy || !x || !rstd || !dx || T < 0 || T > kMaxRows || K <= 0 || K > kNormMaxK || !valid_type(x_type) || !valid_type(w_type))
         return DG_ERR_INVALID_ARG;
     if ((dw || db) && T > 0 && (!workspace || workspace_bytes < dg_layer_norm_backward_workspace(T, K)))
         return DG_ERR_INVALID_ARG;
@@ -257,12 +260,14 @@ dg_status dg_moe_route(const void *logits, const float *bias, int32_t *ids, floa
     p.k = k;
     p.groups = topk_groups == groups ? 1 : groups;   // every group kept: no choice between groups
     p.topk_groups = topk_groups;
+    p.group_size = E / p.groups;
+    p.rows_per_group = p.group_size % 32 == 0 ? p.group_size / 32 : 0;
     p.group_top = group_top;
     p.score = score;
     p.renorm = renorm ? 1 : 0;
     p.scale = scale;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return dtype == DG_BF16 ? run_route<__nv_bfloat16>(p, st) : run_route<float>(p, st);
+    return dtype == DG_BF16 ? run_route<__nv_bfloat16>(p, di->sm_count, st) : run_route<float>(p, di->sm_count, st);
 }
 
 dg_status dg_moe_route_backward(const float *grad_weights, const void *logits, const int32_t *ids, void *grad_logits,
@@ -342,7 +347,7 @@ dg_status dg_cast_fp8_per_token_scatter_topk(const void *x, const int32_t *dst_r
 
 dg_status dg_moe_combine(const void *d, const int32_t *dst_rows, const float *weights, const void *c, void *y, int T,
                          int k, int N, int R, void *stream) {
-    if ((R > 0 && !d) || (T > 0 && (!dst_rows || !y)) || T < 0 || k <= 0 || k > dg::COMBINE_MAX_K || N <= 0 || N % 8 != 0 || R < 0)
+    if ((R > 0 && !d) || (T > 0 && (!dst_rows || !y)) || T < 0 || T > kMaxRows || k <= 0 || k > dg::COMBINE_MAX_K || N <= 0 || N % 8 != 0 || R < 0)
         return DG_ERR_INVALID_ARG;
     if (!aligned16(d) || !aligned16(c) || !aligned16(y)) return DG_ERR_ALIGNMENT;
     if (T == 0) return DG_OK;
@@ -370,7 +375,7 @@ dg_status dg_moe_combine_backward(const void *grad_y, const void *d, const int32
                                   const int32_t *grouped_layout, void *grad_d, float *grad_weights, int T, int k, int N,
                                   int R, void *stream) {
     if ((T > 0 && (!grad_y || !dst_rows)) || (T > 0 && R > 0 && !grad_d && !grad_weights) ||
-        (R > 0 && grad_weights && !d) || (grouped_layout && !grad_d) || T < 0 || k <= 0 || k > dg::COMBINE_MAX_K || N <= 0 || N % 8 != 0 || R < 0)
+        (R > 0 && grad_weights && !d) || (grouped_layout && !grad_d) || T < 0 || T > kMaxRows || k <= 0 || k > dg::COMBINE_MAX_K || N <= 0 || N % 8 != 0 || R < 0)
         return DG_ERR_INVALID_ARG;
     if (!aligned16(grad_y) || !aligned16(d) || !aligned16(grad_d)) return DG_ERR_ALIGNMENT;
     const DeviceInfo *di = nullptr;

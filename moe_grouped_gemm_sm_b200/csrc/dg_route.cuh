@@ -33,6 +33,7 @@ struct RouteParams {
     void *grad_logits;      // backward: [T,E]
     int *err;
     int T, E, k, groups, topk_groups, group_top, score, renorm;
+    int group_size, rows_per_group;   // E / groups; the same over 32, or 0 if that is not whole
     float scale;
 };
 
@@ -55,10 +56,10 @@ __device__ __forceinline__ float sigmoid_scaled(float x, float m) {
     return x >= 0.f ? 1.f / (1.f + expf(-x)) : expf(x - m) / (1.f + expf(x));
 }
 
-__device__ __forceinline__ double sigmoid_f64(double x) {
-    if (x >= 0.0) return 1.0 / (1.0 + exp(-x));
-    const double e = exp(x);
-    return e / (1.0 + e);
+// The score of a logit in 64 bits (softmax: from the row's largest logit and sum).
+__device__ __noinline__ double route_score_f64(double x, double mx, double sum, bool softmax) {
+    const double e = exp(softmax ? x - mx : -fabs(x));   // sigmoid: of -|x|, so that nothing overflows
+    return (softmax || x < 0.0 ? e : 1.0) / (softmax ? sum : 1.0 + e);
 }
 
 // Weights of the chosen logits, one per lane (`in`: the lane holds one). `row_max`, `row_sum`: of
@@ -77,135 +78,449 @@ __device__ __forceinline__ float route_weight(const RouteParams &p, float scale,
     return in ? scale * (s / sum) : 0.f;
 }
 
-// A warp per token; lane l holds the experts l, l + 32, ... (EPL of them) in registers.
-// Values that decide the choice are 64-bit: two scores that differ by less than an fp32 rounding
-// keep the order of their real values.
-template <typename LT, int EPL>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(const RouteParams p) {
-    pdl_launch_dependents();
-    pdl_wait();
+// 64-bit values as integers in the same order; 0 stands for "out of the choice" (-inf).
+__device__ __forceinline__ uint64_t order_key(double v) {
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));   // -0 and 0 are the same
+    return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double key_value(uint64_t k) {
+    if (k == 0) return -CUDART_INF;
+    return __longlong_as_double(static_cast<long long>(k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
+}
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
+    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(k >> 32));
+    const uint32_t lo =
+        __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+// The 64-bit choice value of expert e with logit x (0: out of the choice).
+template <typename LT>
+__device__ __forceinline__ uint64_t route_key_f64(const RouteParams &p, const LT *row, int e, float mx, double sum) {
+    const float x = route_logit(static_cast<float>(row[e]), nullptr);
+    if (!(x > -CUDART_INF_F)) return 0;
+    if (!p.bias) return order_key(static_cast<double>(x));
+    const float b = p.bias[e];
+    if (!(b > -CUDART_INF_F)) return 0;
+    return order_key(route_score_f64(x, mx, sum, p.score == SCORE_SOFTMAX) + static_cast<double>(b));
+}
+
+// The row's largest logit and its 64-bit sum of exp(x - largest), for softmax.
+template <typename LT>
+__device__ __noinline__ double route_sum_f64(const RouteParams &p, const LT *row, float mx) {
+    double sum = 0.0;
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < p.E; e += 32) {
+        const float x = route_logit(static_cast<float>(row[e]), nullptr);
+        if (x > -CUDART_INF_F) sum += exp(static_cast<double>(x) - static_cast<double>(mx));
+    }
+#pragma unroll 1
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    return sum;
+}
+
+// The 64-bit value of group g, the same in every lane: the sum of its group_top largest choice values.
+template <typename LT>
+__device__ __noinline__ double route_group_f64(const RouteParams &p, const LT *row, int g, float mx, double sum) {
     const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * ROUTE_WARPS + (threadIdx.x >> 5);
-    if (t >= p.T) return;
+    uint64_t a = 0, b = 0;   // the lane's two largest
+#pragma unroll 1
+    for (int q = lane; q < p.group_size; q += 32) {
+        const uint64_t c = route_key_f64(p, row, g * p.group_size + q, mx, sum);
+        b = max(b, min(a, c));
+        a = max(a, c);
+    }
+    const uint64_t k1 = warp_max_key(a);
+    const int first = __ffs(__ballot_sync(0xFFFFFFFFu, a == k1)) - 1;
+    const uint64_t k2 = p.group_top == 2 ? warp_max_key(lane == first ? b : a) : 0;
+    double v1 = key_value(k1), v2 = key_value(k2);
+    if (!p.bias && p.group_top == 2 && k1) {   // back from logits to scores
+        v1 = route_score_f64(v1, mx, sum, p.score == SCORE_SOFTMAX);
+        if (k2) v2 = route_score_f64(v2, mx, sum, p.score == SCORE_SOFTMAX);
+    }
+    return k2 ? v1 + v2 : v1;
+}
+
+// One token by a warp with every value that decides the choice in 64 bits; lane l holds the
+// experts l, l + 32, .... Taken for k > 30 and where more than 31 candidates lie too close together
+// for fp32 (rows of equal fp32 logits, say). Rolled loops over a local array keep the code short: it is rarely in the instruction
+// cache, and unrolled it took 12 us for a single token, most of it fetching instructions.
+template <typename LT>
+__device__ __noinline__ void route_token_f64(const RouteParams &p, int t) {
+    const int lane = threadIdx.x & 31, n = (p.E + 31) / 32;
     const LT *row = static_cast<const LT *>(p.logits) + static_cast<size_t>(t) * p.E;
-    float x[EPL];
-    float mx = -CUDART_INF_F;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = i * 32 + lane;
-        x[i] = e < p.E ? route_logit(static_cast<float>(row[e]), p.err) : -CUDART_INF_F;
-        mx = fmaxf(mx, x[i]);
-    }
     const bool softmax = p.score == SCORE_SOFTMAX;
-    float sum = 0.f;
-    double sum64 = 0.0;
+    uint64_t c[ROUTE_MAX_E / 32];
+    float mx = -CUDART_INF_F;
+    double sum = 1.0;
     if (softmax) {
+#pragma unroll 1
+        for (int e = lane; e < p.E; e += 32) mx = fmaxf(mx, route_logit(static_cast<float>(row[e]), nullptr));
         mx = warp_max(mx);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (x[i] > -CUDART_INF_F) sum += expf(x[i] - mx);
-        sum = warp_sum(sum);
-        if (p.bias) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (x[i] > -CUDART_INF_F) sum64 += exp(static_cast<double>(x[i]) - static_cast<double>(mx));
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum64 += __shfl_xor_sync(0xFFFFFFFFu, sum64, o);
-        }
+        sum = route_sum_f64(p, row, mx);
     }
-    // choice values: the score plus the bias; without a bias the logit itself, which is in the
-    // same order as its score
-    double c[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = i * 32 + lane;
-        c[i] = x[i];
-        if (p.bias && x[i] > -CUDART_INF_F) {
-            const float b = p.bias[e];
-            if (b != b) report_error(p.err, ERR_DATA);
-            const double s = softmax ? exp(static_cast<double>(x[i]) - static_cast<double>(mx)) / sum64
-                                     : sigmoid_f64(static_cast<double>(x[i]));
-            c[i] = b > -CUDART_INF_F ? s + static_cast<double>(b) : -CUDART_INF;
-        }
-    }
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) c[i] = i * 32 + lane < p.E ? route_key_f64(p, row, i * 32 + lane, mx, sum) : 0;
     if (p.groups > 1) {
-        const int gs = p.E / p.groups;
+        const int gs = p.group_size;
         double mine = -CUDART_INF;   // lane g: the value of group g
+#pragma unroll 1
         for (int g = 0; g < p.groups; ++g) {
-            double a = -CUDART_INF, b = -CUDART_INF;   // the two largest
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const int e = i * 32 + lane;
-                if (e >= g * gs && e < (g + 1) * gs) {
-                    b = fmax(b, fmin(a, c[i]));
-                    a = fmax(a, c[i]);
-                }
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) {
-                const double a2 = __shfl_xor_sync(0xFFFFFFFFu, a, o), b2 = __shfl_xor_sync(0xFFFFFFFFu, b, o);
-                b = fmax(fmin(a, a2), fmax(b, b2));
-                a = fmax(a, a2);
-            }
-            double v = a;
-            if (p.group_top == 2 && a > -CUDART_INF) {
-                if (!p.bias) {   // back from logits to scores (softmax: times the row's sum)
-                    a = softmax ? exp(a - static_cast<double>(mx)) : sigmoid_f64(a);
-                    if (b > -CUDART_INF) b = softmax ? exp(b - static_cast<double>(mx)) : sigmoid_f64(b);
-                }
-                v = b > -CUDART_INF ? a + b : a;
-            }
+            const double v = route_group_f64(p, row, g, mx, sum);
             if (lane == g) mine = v;
         }
         int rank = 0;
+#pragma unroll 1
         for (int h = 0; h < p.groups; ++h) {
             const double v = __shfl_sync(0xFFFFFFFFu, mine, h);
             rank += (v > mine || (v == mine && h < lane)) ? 1 : 0;
         }
         const uint32_t kept = __ballot_sync(0xFFFFFFFFu, lane < p.groups && rank < p.topk_groups);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
             const int e = i * 32 + lane;
-            if (e < p.E && !((kept >> (e / gs)) & 1u)) c[i] = -CUDART_INF;
+            if (e < p.E && !((kept >> (e / gs)) & 1u)) c[i] = 0;
         }
     }
-    int my_id = -1;
-    float my_x = 0.f;
+    int id = -1;
+#pragma unroll 1
     for (int j = 0; j < p.k; ++j) {
-        double best = -CUDART_INF;
-        int e = -1;
-        float xe = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
+        uint64_t best = 0;
+        int at = 0;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i)
             if (c[i] > best) {
                 best = c[i];
-                e = i * 32 + lane;
-                xe = x[i];
+                at = i;
             }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            const double b2 = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-            const int e2 = __shfl_xor_sync(0xFFFFFFFFu, e, o);
-            const float x2 = __shfl_xor_sync(0xFFFFFFFFu, xe, o);
-            if (b2 > best || (b2 == best && e2 < e)) {
-                best = b2;
-                e = e2;
-                xe = x2;
-            }
-        }
-        if (best == -CUDART_INF) break;   // the same in every lane
-        if (lane == j) {
-            my_id = e;
-            my_x = xe;
-        }
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (i * 32 + lane == e) c[i] = -CUDART_INF;
+        const uint64_t m = warp_max_key(best);
+        if (m == 0) break;   // the same in every lane
+        const uint32_t mine = best == m ? static_cast<uint32_t>(at * 32 + lane) : 0xFFFFFFFFu;
+        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, mine);
+        if (mine == e) c[at] = 0;
+        if (lane == j) id = static_cast<int>(e);
     }
-    const float w = route_weight(p, p.scale, my_id >= 0, my_x, mx, sum);
+    const float x = id >= 0 ? fminf(static_cast<float>(row[id]), CUDART_MAX_NORMAL_F) : 0.f;
+    const float w = route_weight(p, p.scale, id >= 0, x, mx, static_cast<float>(sum));
     if (lane < p.k) {
-        p.ids[static_cast<size_t>(t) * p.k + lane] = my_id;
+        p.ids[static_cast<size_t>(t) * p.k + lane] = id;
         p.weights[static_cast<size_t>(t) * p.k + lane] = w;
+    }
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float redux_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float sigmoid_approx(float x) { return rcp_approx(1.f + ex2_approx(-1.44269504f * x)); }
+
+// Falling order, by a bitonic network.
+template <int N>
+__device__ __forceinline__ void sort_falling(float (&v)[N]) {
+#pragma unroll
+    for (int k = 2; k <= N; k *= 2)
+#pragma unroll
+        for (int j = k / 2; j > 0; j /= 2)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int l = i ^ j;
+                if (l > i) {
+                    const float hi = fmaxf(v[i], v[l]), lo = fminf(v[i], v[l]);
+                    const bool falling = (i & k) == 0;
+                    v[i] = falling ? hi : lo;
+                    v[l] = falling ? lo : hi;
+                }
+            }
+}
+
+// One token by a warp; lane l holds the experts i·32 + l. True: it has to be done again in 64 bits.
+//
+// Choice values are fp32 from the hardware's exponential and reciprocal. The low log2(EPL) bits of a
+// value are replaced by the register index i (inverted for values >= 0), so that the value names
+// its expert: a lane sorts plain floats, and each choice is one maximum over the lanes' first
+// values, a ballot for the lowest lane that has it, and a shift of that lane's values. Equal
+// values then come in the order of their expert's index.
+// Two values whose distance is within the errors (packing: EPL·2^-23 of each; sigmoid: 2^-21.5 of 1; softmax:
+// 2^-18 of the largest score, from the sum) might stand in the other order, or one might be
+// chosen wrongly: then all that may belong to the k largest, one in a lane, are put in the order of
+// their 64-bit values, and groups at the border likewise. Neighbours with the same logit and the
+// same bias are equal in truth and need no second look. With N(0,1.5) logits over 256 experts that
+// is about one token in 300.
+template <typename LT, int EPL>
+__device__ __forceinline__ bool route_token(const RouteParams &p, const float (&b)[EPL], int t, int lane) {
+    const bool softmax = p.score == SCORE_SOFTMAX, by_logit = p.bias == nullptr;
+    const int E = p.E, k = p.k;
+    const LT *row = static_cast<const LT *>(p.logits) + static_cast<size_t>(t) * E;
+    float c[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = i * 32 + lane;
+        c[i] = e < E ? static_cast<float>(row[e]) : -CUDART_INF_F;
+    }
+    // a sum that is not finite: some logit is not, or there are fewer than 32·EPL of them
+    float mx = c[0], acc = c[0], sum = 1.f;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) {
+        acc += c[i];
+        mx = fmaxf(mx, c[i]);
+    }
+    const bool holes = !(fabsf(acc) <= CUDART_MAX_NORMAL_F);
+    if (holes) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            bad |= c[i] != c[i];
+            c[i] = c[i] == c[i] ? fminf(c[i], CUDART_MAX_NORMAL_F) : -CUDART_INF_F;
+        }
+        mx = c[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) mx = fmaxf(mx, c[i]);
+        if (bad) report_error(p.err, ERR_DATA);
+    }
+    if (softmax) {
+        mx = redux_max(mx);
+        if (!by_logit || !p.renorm) {
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (c[i] > -CUDART_INF_F) sum += ex2_approx(1.44269504f * (c[i] - mx));
+            sum = warp_sum(sum);
+        }
+    }
+    const float top = softmax ? rcp_approx(sum) : 1.f;   // no score is larger
+    if (!by_logit) {
+        if (softmax) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                c[i] = c[i] > -CUDART_INF_F ? fmaf(top, ex2_approx(1.44269504f * (c[i] - mx)), b[i]) : -CUDART_INF_F;
+        } else if (holes) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = c[i] > -CUDART_INF_F ? sigmoid_approx(c[i]) + b[i] : -CUDART_INF_F;
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) c[i] = sigmoid_approx(c[i]) + b[i];
+        }
+    }
+    const float tol_score = softmax ? top * 0x1p-17f : 0x1p-20f;
+    if (p.groups > 1) {
+        float a1 = -CUDART_INF_F, a2 = -CUDART_INF_F;   // lane g: the two largest of group g
+        if (p.rows_per_group) {
+            // groups of whole registers: first the two largest of each register, in lane i
+            float r1 = -CUDART_INF_F, r2 = -CUDART_INF_F;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const float m1 = redux_max(c[i]);
+                float m2 = m1;
+                if (p.group_top == 2) {
+                    const int first = __ffs(__ballot_sync(0xFFFFFFFFu, c[i] == m1)) - 1;
+                    m2 = redux_max(lane == first ? -CUDART_INF_F : c[i]);
+                }
+                if (lane == i) {
+                    r1 = m1;
+                    r2 = m2;
+                }
+            }
+            if (p.rows_per_group == 1) {
+                a1 = r1;
+                a2 = r2;
+            } else {
+                for (int q = 0; q < p.rows_per_group; ++q) {
+                    const int from = lane * p.rows_per_group + q;
+                    const float v1 = __shfl_sync(0xFFFFFFFFu, r1, from & 31), v2 = __shfl_sync(0xFFFFFFFFu, r2, from & 31);
+                    if (lane < p.groups) {
+                        a2 = fmaxf(fminf(a1, v1), fmaxf(a2, v2));
+                        a1 = fmaxf(a1, v1);
+                    }
+                }
+            }
+        } else {
+            const int gs = p.group_size;
+            for (int g = 0; g < p.groups; ++g) {
+                float l1 = -CUDART_INF_F, l2 = -CUDART_INF_F;
+                const int e0 = g * gs - lane;   // expert i·32 + lane is in the group if i·32 is in [e0, e0 + gs)
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (static_cast<unsigned>(i * 32 - e0) < static_cast<unsigned>(gs)) {
+                        l2 = fmaxf(l2, fminf(l1, c[i]));
+                        l1 = fmaxf(l1, c[i]);
+                    }
+                const float m1 = redux_max(l1);
+                const int first = __ffs(__ballot_sync(0xFFFFFFFFu, l1 == m1)) - 1;
+                const float m2 = redux_max(lane == first ? l2 : l1);
+                if (lane == g) {
+                    a1 = m1;
+                    a2 = m2;
+                }
+            }
+        }
+        const bool sums = !by_logit || p.group_top == 2;   // scores, not logits, decide between the groups
+        if (by_logit && sums && a1 > -CUDART_INF_F) {      // to scores (softmax: times the row's sum)
+            a1 = softmax ? ex2_approx(1.44269504f * (a1 - mx)) : sigmoid_approx(a1);
+            if (a2 > -CUDART_INF_F) a2 = softmax ? ex2_approx(1.44269504f * (a2 - mx)) : sigmoid_approx(a2);
+        }
+        const float mine = p.group_top == 2 && a2 > -CUDART_INF_F ? a1 + a2 : a1;
+        int rank = 0;
+        for (int h = 0; h < p.groups; ++h) {
+            const float v = __shfl_sync(0xFFFFFFFFu, mine, h);
+            rank += (v > mine || (v == mine && h < lane)) ? 1 : 0;
+        }
+        const bool keep = lane < p.groups && rank < p.topk_groups;
+        uint32_t kept = __ballot_sync(0xFFFFFFFFu, keep);
+        if (sums) {
+            // is the border between the groups wide enough? Groups too close to it compete again by
+            // their 64-bit values; the others are truly above or below all of those.
+            const float in = -redux_max(keep ? -mine : -CUDART_INF_F);
+            const float out = redux_max(keep ? -CUDART_INF_F : mine);
+            const float tol = 2.f * (by_logit ? (softmax ? 0x1p-17f : 0x1p-20f) : tol_score) + 0x1p-21f * (fabsf(in) + fabsf(out));
+            if (out > -CUDART_INF_F && !(in - out > tol)) {
+                const bool open = lane < p.groups && !(keep ? mine - out > tol : in - mine > tol);
+                const uint32_t compete = __ballot_sync(0xFFFFFFFFu, open);
+                const double sum64 = softmax && !by_logit ? route_sum_f64(p, row, mx) : 1.0;
+                double exact = -CUDART_INF;
+                for (uint32_t left = compete; left; left &= left - 1) {
+                    const int g = __ffs(left) - 1;
+                    const double v = route_group_f64(p, row, g, mx, sum64);
+                    if (lane == g) exact = v;
+                }
+                int before = __popc(kept & ~compete);
+                for (uint32_t left = compete; left; left &= left - 1) {
+                    const int h = __ffs(left) - 1;
+                    const double v = __shfl_sync(0xFFFFFFFFu, exact, h);
+                    before += (v > exact || (v == exact && h < lane)) ? 1 : 0;
+                }
+                kept = __ballot_sync(0xFFFFFFFFu, open ? before < p.topk_groups : keep);
+            }
+        }
+        if (p.rows_per_group == 1) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (!((kept >> i) & 1u)) c[i] = -CUDART_INF_F;
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int e = i * 32 + lane;
+                if (e < E && !((kept >> (e / p.group_size)) & 1u)) c[i] = -CUDART_INF_F;
+            }
+        }
+    }
+    if (EPL > 1) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const uint32_t u = __float_as_uint(c[i] + 0.f);   // + 0: -0 and 0 are the same
+            const uint32_t low = (~static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) & (EPL - 1)) ^ i;
+            if (c[i] > -CUDART_INF_F) c[i] = __uint_as_float((u & ~static_cast<uint32_t>(EPL - 1)) | low);
+        }
+        sort_falling<EPL>(c);
+    }
+    float v = -CUDART_INF_F;   // lane j: the j-th largest
+    int from = 0;
+    // lane `at` takes the largest value that is left, and its lane's values move up
+    const auto take = [&](int at) {
+        const float m = redux_max(c[0]);
+        const int f = __ffs(__ballot_sync(0xFFFFFFFFu, c[0] == m)) - 1;
+        if (lane == at) {
+            v = m;
+            from = f;
+        }
+        if (lane == f) {
+#pragma unroll
+            for (int i = 0; i + 1 < EPL; ++i) c[i] = c[i + 1];
+            c[EPL - 1] = -CUDART_INF_F;
+        }
+    };
+    for (int j = 0; j <= k; ++j) take(j);   // lane k: the best that is left out
+    const auto expert = [&] {
+        const uint32_t u = __float_as_uint(v);
+        return v > -CUDART_INF_F
+                   ? static_cast<int>((~static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) ^ u) & (EPL - 1)) * 32 + from
+                   : -1;
+    };
+    int id = expert(), place = lane;
+    float xs = id >= 0 ? fminf(static_cast<float>(row[id]), CUDART_MAX_NORMAL_F) : 0.f;
+    if (!(sizeof(LT) == 2 && by_logit && EPL <= 32)) {   // bf16 logits have the bits to spare: their order is exact
+        const float bs = id >= 0 && !by_logit ? p.bias[id] : 0.f;
+        const float v1 = __shfl_down_sync(0xFFFFFFFFu, v, 1), x1 = __shfl_down_sync(0xFFFFFFFFu, xs, 1);
+        const float b1 = __shfl_down_sync(0xFFFFFFFFu, bs, 1);
+        const float tol = (by_logit ? 0x1p-120f : tol_score) + EPL * 0x1p-22f * fabsf(v);
+        const bool near = lane < k && v1 > -CUDART_INF_F && v - v1 <= tol;
+        bool again = near && !(by_logit ? xs >= x1 : xs == x1 && bs == b1);
+        // near the border: what comes behind the best one left out must be far, too
+        if (__ballot_sync(0xFFFFFFFFu, near) >> (k - 1) & 1u) {
+            const float v2 = redux_max(c[0]);
+            again |= lane == k - 1 && v2 > -CUDART_INF_F && v - v2 <= tol;
+        }
+        if (__any_sync(0xFFFFFFFFu, again)) {
+            // all values that may belong to the k largest, then their order by the 64-bit values
+            const float last = __shfl_sync(0xFFFFFFFFu, v - tol, k - 1);
+            int n = k + 1;
+            for (; n < 32 && redux_max(c[0]) >= last; ++n) take(n);
+            if (redux_max(c[0]) >= last && last > -CUDART_INF_F) return true;   // still more of them
+            id = expert();
+            xs = id >= 0 ? fminf(static_cast<float>(row[id]), CUDART_MAX_NORMAL_F) : 0.f;
+            const double sum64 = softmax && !by_logit ? route_sum_f64(p, row, mx) : 1.0;
+            const uint64_t key = id >= 0 ? route_key_f64(p, row, id, mx, sum64) : 0;
+            place = 0;
+            for (int j = 0; j < n; ++j) {
+                const uint64_t kj = __shfl_sync(0xFFFFFFFFu, key, j);
+                const int idj = __shfl_sync(0xFFFFFFFFu, id, j);
+                place += (kj > key || (kj == key && idj < id)) ? 1 : 0;
+            }
+            if (id < 0) place = lane < n ? lane : 32;   // behind all the others already
+        }
+    }
+    const bool out = place < k;
+    if (!out) id = -1;
+    const float w = route_weight(p, p.scale, id >= 0, xs, mx, sum);
+    if (out) {
+        p.ids[static_cast<size_t>(t) * k + place] = id;
+        p.weights[static_cast<size_t>(t) * k + place] = w;
+    }
+    return false;
+}
+
+// Tokens in batches of up to 32 per warp, then the batch's tokens that are done again: the 64-bit
+// form is a call, and nothing of the fp32 form has to live across it.
+template <typename LT, int EPL>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS, EPL <= 8 ? 8 : 1) route_kernel(const __grid_constant__ RouteParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, step = gridDim.x * ROUTE_WARPS;
+    for (long long t0 = blockIdx.x * ROUTE_WARPS + (threadIdx.x >> 5); t0 < p.T; t0 += 32LL * step) {
+        uint32_t redo = 0;
+        {
+            float b[EPL];
+            if (p.bias) {
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const int e = i * 32 + lane;
+                    b[i] = e < p.E ? p.bias[e] : -CUDART_INF_F;
+                    if (b[i] != b[i]) report_error(p.err, ERR_DATA);
+                    // +inf: the largest finite value, which has bits to spare for the index
+                    b[i] = b[i] == b[i] ? fminf(b[i], CUDART_MAX_NORMAL_F) : -CUDART_INF_F;
+                }
+            }
+            for (int n = 0; n < 32; ++n) {
+                const long long t = t0 + static_cast<long long>(n) * step;
+                if (t >= p.T) break;
+                if (p.k > 30 || route_token<LT, EPL>(p, b, static_cast<int>(t), lane)) redo |= 1u << n;
+            }
+        }
+        while (redo) {
+            const int n = __ffs(redo) - 1;
+            redo &= redo - 1;
+            route_token_f64<LT>(p, static_cast<int>(t0 + static_cast<long long>(n) * step));
+        }
     }
 }
 

@@ -194,19 +194,19 @@ _HERE = contextlib.nullcontext()
 
 
 def _check(name, t, shape=None, dtype=None, device=None):
-    """A contiguous CUDA tensor of this shape and dtype (or one of these dtypes) on this device."""
+    """A contiguous CUDA tensor of this shape and dtype (or one of these dtypes) on this device (index)."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: a tensor is wanted")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors are on {device}")
-    if dtype is not None and t.dtype != dtype and (isinstance(dtype, torch.dtype) or t.dtype not in dtype):
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on cuda:{device}")
+    if dtype is not None and t.dtype is not dtype and (isinstance(dtype, torch.dtype) or t.dtype not in dtype):
         raise ValueError(f"{name}: dtype {t.dtype}, wanted {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {shape}")
 
 
 def _check_2d(name, t, dtype, device=None):
@@ -217,25 +217,25 @@ def _check_2d(name, t, dtype, device=None):
 
 
 def _on(device, stream):
-    """Makes ``device`` and ``stream`` current: kernels run there, and what is allocated inside
+    """Makes the device (an index) and ``stream`` current: kernels run there, and what is allocated inside
     belongs to that stream, so that a workspace is not handed out again while it is in use."""
     if stream is None:
-        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return _HERE if device == torch.cuda.current_device() else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{device}")
     return torch.cuda.stream(stream)
 
 
 def _norm_args(x, weight, bias, rms):
     T, K = _check_2d("x", x, _TYPES)
     if weight is not None:
-        _check("weight", weight, (K,), _TYPES, x.device)
+        _check("weight", weight, (K,), _TYPES, x.get_device())
     if bias is not None:
         if rms:
             raise ValueError("the RMS form takes no bias")
-        _check("bias", bias, (K,), weight.dtype if weight is not None else _TYPES, x.device)
+        _check("bias", bias, (K,), weight.dtype if weight is not None else _TYPES, x.get_device())
     w = weight if weight is not None else bias
     return T, K, _TYPES[w.dtype] if w is not None else 0
 
@@ -246,8 +246,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, stats=False, out=
     None in the RMS form). ``out`` may be x."""
     T, K, w_type = _norm_args(x, weight, bias, rms)
     if out is not None:
-        _check("out", out, (T, K), x.dtype, x.device)
-    with _on(x.device, stream):
+        _check("out", out, (T, K), x.dtype, x.get_device())
+    with _on(x.get_device(), stream):
         y = out if out is not None else torch.empty_like(x)
         mean = rstd = None
         if stats:
@@ -264,7 +264,7 @@ def layer_norm_cast(x, weight=None, bias=None, eps=1e-5, rms=False, stream=None)
     T, K, w_type = _norm_args(x, weight, bias, rms)
     if K % 128:
         raise ValueError(f"K = {K} is not a multiple of 128")
-    with _on(x.device, stream):
+    with _on(x.get_device(), stream):
         q = torch.empty((T, K), dtype=torch.uint8, device=x.device)
         sfa = (torch.zeros if T % 4 else torch.empty)((K // 128, _pad4(T)), dtype=torch.float32, device=x.device)
         if T:
@@ -276,15 +276,15 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, rms=False, stream=
     """Gradients (dx [T,K] of x's type, dw fp32 [K] or None without a weight, db fp32 [K] or None unless
     ``bias``) of layer_norm from dy and the saved mean and rstd (fp32 [T]; mean None in the RMS form)."""
     T, K, w_type = _norm_args(x, weight, None, rms)
-    _check("dy", dy, (T, K), x.dtype, x.device)
-    _check("rstd", rstd, (T,), torch.float32, x.device)
+    _check("dy", dy, (T, K), x.dtype, x.get_device())
+    _check("rstd", rstd, (T,), torch.float32, x.get_device())
     if (mean is None) != bool(rms):
         raise ValueError("mean is wanted unless rms")
     if mean is not None:
-        _check("mean", mean, (T,), torch.float32, x.device)
+        _check("mean", mean, (T,), torch.float32, x.get_device())
     if rms and bias:
         raise ValueError("the RMS form has no bias")
-    with _on(x.device, stream):
+    with _on(x.get_device(), stream):
         dx = torch.empty_like(x)
         dw = torch.empty(K, dtype=torch.float32, device=x.device) if weight is not None else None
         db = torch.empty(K, dtype=torch.float32, device=x.device) if bias else None
@@ -312,9 +312,9 @@ def moe_route(logits, k, bias=None, groups=1, topk_groups=1, group_top=1, score=
     weight. Places that no expert fills hold id -1 and weight 0."""
     T, E = _check_2d("logits", logits, _TYPES)
     if bias is not None:
-        _check("bias", bias, (E,), torch.float32, logits.device)
+        _check("bias", bias, (E,), torch.float32, logits.get_device())
     s = _score(score)
-    with _on(logits.device, stream):
+    with _on(logits.get_device(), stream):
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
         weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
         if T:
@@ -326,11 +326,11 @@ def moe_route(logits, k, bias=None, groups=1, topk_groups=1, group_top=1, score=
 def moe_route_backward(grad_weights, logits, ids, score="softmax", renorm=True, scale=1.0, stream=None):
     """Gradient of the logits (of their type) from the gradient of moe_route's weights (fp32 [T,k])."""
     T, E = _check_2d("logits", logits, _TYPES)
-    _, k = _check_2d("ids", ids, torch.int32, logits.device)
+    _, k = _check_2d("ids", ids, torch.int32, logits.get_device())
     _check("ids", ids, (T, k))
-    _check("grad_weights", grad_weights, (T, k), torch.float32, logits.device)
+    _check("grad_weights", grad_weights, (T, k), torch.float32, logits.get_device())
     s = _score(score)
-    with _on(logits.device, stream):
+    with _on(logits.get_device(), stream):
         g = torch.empty_like(logits)
         if T:
             _lib.dg_moe_route_backward(grad_weights, logits, ids, g, T, E, k, s, int(renorm), scale, _TYPES[logits.dtype])
@@ -349,10 +349,10 @@ def moe_layout_contiguous(ids, G, M_sum=None, stream=None):
     T, k = _check_2d("ids", ids, torch.int32)
     if M_sum is None:
         M_sum = (T * k + 127 * min(G, T * k) + 127) // 128 * 128
-    with _on(ids.device, stream):
+    with _on(ids.get_device(), stream):
         dst = torch.empty_like(ids)
-        layout = torch.empty(M_sum, dtype=torch.int32, device=ids.device)
-        ks = torch.empty(G, dtype=torch.int32, device=ids.device)
+        layout = ids.new_empty(M_sum)
+        ks = ids.new_empty(G)
         ws, need = _layout_workspace(T, k, G, ids.device)
         _lib.dg_moe_layout_contiguous(ids, dst, layout, ks, ws, need, T, k, G, M_sum)
     return dst, layout, ks
@@ -362,9 +362,9 @@ def moe_layout_masked(ids, G, M_max, stream=None):
     """Rows of the masked layout for expert ids int32 [T,k] (ids outside [0,G) are dropped):
     (dst_rows int32 [T,k] with row g·M_max + i for expert g's i-th token, masked_m int32 [G])."""
     T, k = _check_2d("ids", ids, torch.int32)
-    with _on(ids.device, stream):
+    with _on(ids.get_device(), stream):
         dst = torch.empty_like(ids)
-        masked_m = torch.empty(G, dtype=torch.int32, device=ids.device)
+        masked_m = ids.new_empty(G)
         ws, need = _layout_workspace(T, k, G, ids.device)
         _lib.dg_moe_layout_masked(ids, dst, masked_m, ws, need, T, k, G, M_max)
     return dst, masked_m
@@ -375,14 +375,14 @@ def cast_per_token_scatter_topk(x, dst_rows, M, G=1, out=None, stream=None):
     rows (contiguous: G = 1, M = M_sum; masked: M = M_max): (e4m3 [G·M,K], sfa fp32 [G,Kb,pad4(M)]).
     Rows no token maps to are zero, or keep what ``out`` = (q, sfa) held."""
     T, K = _check_2d("x", x, torch.bfloat16)
-    _, k = _check_2d("dst_rows", dst_rows, torch.int32, x.device)
+    _, k = _check_2d("dst_rows", dst_rows, torch.int32, x.get_device())
     _check("dst_rows", dst_rows, (T, k))
     if K % 128:
         raise ValueError(f"K = {K} is not a multiple of 128")
     if out is not None:
-        _check("out[0]", out[0], (G * M, K), torch.uint8, x.device)
-        _check("out[1]", out[1], (G, K // 128, _pad4(M)), torch.float32, x.device)
-    with _on(x.device, stream):
+        _check("out[0]", out[0], (G * M, K), torch.uint8, x.get_device())
+        _check("out[1]", out[1], (G, K // 128, _pad4(M)), torch.float32, x.get_device())
+    with _on(x.get_device(), stream):
         q, sfa = out if out is not None else (
             torch.zeros((G * M, K), dtype=torch.uint8, device=x.device),
             torch.zeros((G, K // 128, _pad4(M)), dtype=torch.float32, device=x.device))
@@ -396,16 +396,16 @@ def moe_combine(d, dst_rows, weights=None, c=None, out=None, stream=None):
     shape; negative rows are left out). ``out`` may be c. Without weights (ones) this is also the
     gradient of the dispatch."""
     _check("d", d, None, torch.bfloat16)
-    T, k = _check_2d("dst_rows", dst_rows, torch.int32, d.device)
+    T, k = _check_2d("dst_rows", dst_rows, torch.int32, d.get_device())
     N = d.shape[-1]
     if weights is not None:
-        _check("weights", weights, (T, k), torch.float32, d.device)
+        _check("weights", weights, (T, k), torch.float32, d.get_device())
     if c is not None:
-        _check("c", c, (T, N), torch.bfloat16, d.device)
+        _check("c", c, (T, N), torch.bfloat16, d.get_device())
     if out is not None:
-        _check("out", out, (T, N), torch.bfloat16, d.device)
-    with _on(d.device, stream):
-        y = out if out is not None else torch.empty((T, N), dtype=torch.bfloat16, device=d.device)
+        _check("out", out, (T, N), torch.bfloat16, d.get_device())
+    with _on(d.get_device(), stream):
+        y = out if out is not None else d.new_empty((T, N))
         if T:
             _lib.dg_moe_combine(d, dst_rows, weights, c, y, T, k, N, d.numel() // max(N, 1))
     return y
@@ -416,15 +416,15 @@ def moe_combine_backward(grad_y, d, dst_rows, weights=None, grouped_layout=None,
     maps to: with grouped_layout (int32 [M_sum]) its negative rows are zero and every other row has a
     pair; without it all of them are zero."""
     _check("d", d, None, torch.bfloat16)
-    T, k = _check_2d("dst_rows", dst_rows, torch.int32, d.device)
+    T, k = _check_2d("dst_rows", dst_rows, torch.int32, d.get_device())
     N = d.shape[-1]
     R = d.numel() // max(N, 1)
-    _check("grad_y", grad_y, (T, N), torch.bfloat16, d.device)
+    _check("grad_y", grad_y, (T, N), torch.bfloat16, d.get_device())
     if weights is not None:
-        _check("weights", weights, (T, k), torch.float32, d.device)
+        _check("weights", weights, (T, k), torch.float32, d.get_device())
     if grouped_layout is not None:
-        _check("grouped_layout", grouped_layout, (R,), torch.int32, d.device)
-    with _on(d.device, stream):
+        _check("grouped_layout", grouped_layout, (R,), torch.int32, d.get_device())
+    with _on(d.get_device(), stream):
         gd = (torch.zeros_like if grouped_layout is None else torch.empty_like)(d)
         gw = torch.empty((T, k), dtype=torch.float32, device=d.device)
         if T or (R and grouped_layout is not None):

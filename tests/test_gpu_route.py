@@ -275,3 +275,29 @@ def test_refusals():
                  lambda: ops.moe_route(x, 2, scale=float("nan"))):
         with pytest.raises(_lib.DgError):
             call()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,topk_groups,top", [(64, 1, 1, 1), (256, 8, 4, 2), (40, 4, 2, 2), (1024, 1, 1, 1), (128, 4, 2, 1)])
+def test_gaps_of_every_size(score, E, groups, topk_groups, top):
+    """Neighbouring choice values at distances from 1e-9 to 1e-2, and zeros of both signs: whatever precision the
+    first look at a token has, the choice is the definition's."""
+    g = torch.Generator().manual_seed(E)
+    T, half = 160, E // 2
+    x = torch.randn(T, E, generator=g)
+    gap = 10.0 ** (-9 + 7 * torch.rand(T, half, generator=g, dtype=torch.float64)) * torch.randn(T, half, generator=g).sign()
+    perm = torch.randperm(E, generator=g)
+    x[:, perm[half:2 * half]] = (x[:, perm[:half]].double() + gap).float()
+    x[:8, ::3] = 0.0
+    x[:8, 1::3] = -0.0
+    x[8:12] *= 1e-39                              # subnormal logits
+    b = 0.1 * torch.randn(E, generator=g)
+    b[perm[half:2 * half]] = b[perm[:half]]       # the gap is the logits' alone
+    for bias in (b, None, torch.zeros(E)):
+        check(x, bias, 8, groups, topk_groups, top, score)
+        check(x, bias, 30, groups, topk_groups, top, score)
+    b2 = b.clone()
+    b2[:3] = float("inf")
+    b2[3] = FMAX
+    check(x[12:], b2, 8, score=score)
+    assert _lib.dg_get_device_error() == _lib.DG_OK
