@@ -79,6 +79,78 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// Two fp32 values in one register pair, for the packed fp32 instructions (each half rounded as the
+// scalar instruction rounds): they halve the arithmetic instructions of the row kernels.
+struct Pair {
+    uint64_t v;
+};
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float2 halves(Pair p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+    return f;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void load_pairs(const T *p, Pair *f) {
+    float s[V];
+    load_vec<T, V>(p, s);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) f[e] = pair(s[2 * e], s[2 * e + 1]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T *p, const Pair *f) {
+    float s[V];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+        const float2 h = halves(f[e]);
+        s[2 * e] = h.x;
+        s[2 * e + 1] = h.y;
+    }
+    store_vec<T, V>(p, s);
+}
+
+// The warp's sums of a and of b, in every lane: halves of the warp take one value each after the
+// first exchange.
+__device__ __forceinline__ float2 warp_sum2(float a, float b) {
+    const bool up = (threadIdx.x & 16) != 0;
+    float v = (up ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+    return up ? make_float2(w, v) : make_float2(v, w);
+}
+
+// The warp's sums of the four parts of v: lane 8·i holds the i-th.
+__device__ __forceinline__ float warp_sum4_spread(float4 v) {
+    const bool up = (threadIdx.x & 16) != 0, up8 = (threadIdx.x & 8) != 0;
+    const float a = (up ? v.z : v.x) + __shfl_xor_sync(0xFFFFFFFFu, up ? v.x : v.z, 16);
+    const float b = (up ? v.w : v.y) + __shfl_xor_sync(0xFFFFFFFFu, up ? v.y : v.w, 16);
+    float s = (up8 ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, up8 ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    return s;
+}
+
 // Sum over the blockDim.x threads of a row, the same bits in every thread. One warp a row needs no
 // barrier; otherwise the row is the whole block and `red` (32 floats) must not be in use.
 __device__ __forceinline__ float row_sum(float v, float *red) {
@@ -103,6 +175,24 @@ struct NormParams {
     int T, K, ld, rms;
     float eps;
 };
+
+// The cast epilogue of vector i of a row: the 128 / V threads that hold one 1x128 slice take its amax (m:
+// the vector's) by shuffles, so all lanes of a warp call it. The codes are those of the unrounded
+// fp32 values (one rounding instead of two).
+template <int V>
+__device__ __forceinline__ void norm_cast(const NormParams &p, const float (&f)[V], float m, long long row, int i, int nv) {
+#pragma unroll
+    for (int o = 64 / V; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (i >= nv) return;
+    const float sc = scale_of(m);
+    uint8_t *q = p.q + static_cast<size_t>(row) * p.K + static_cast<size_t>(i) * V;
+    if constexpr (V == 8)
+        *reinterpret_cast<uint2 *>(q) = quant8(f, sc);
+    else
+        *reinterpret_cast<uint32_t *>(q) = quant4(f, sc);
+    constexpr int per = 128 / V;
+    if (i % per == 0) p.sfa[static_cast<size_t>(i / per) * p.ld + row] = sc;
+}
 
 // One row of K elements per blockDim.x threads (blockDim.y rows per block, one warp each when
 // blockDim.y > 1). Thread t holds the vectors t, t + blockDim.x, ... of V elements in registers: x is
@@ -177,17 +267,292 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) layer_norm_kernel(const Norm
                 float m = 0.f;
 #pragma unroll
                 for (int e = 0; e < V; ++e) m = fmaxf(m, fabsf(f[j][e]));
+                norm_cast<V>(p, f[j], m, row, i, nv);
+            }
+        }
+    }
+}
+
+// Rows in a ring of shared memory per team of threads, for many rows. blockDim.x threads (a team) share a
+// row; every thread owns N columns of it (NormColumns), the same ones for every row that its team takes.
+// blockDim.y > 1 teams of one warp each serve short rows. The ring has NORM_STAGES stages of R rows (of one or
+// two tensors) and is filled two stages ahead by cp.async; R rows share their barriers.
+// COLS_VECTORS: K is a whole number of 16-byte vectors; a thread owns vectors of V columns, copies and reads its own
+// only, and the ring needs no barrier. COLS_EXACT: and K = N·blockDim.x, so that nothing needs a bounds check (the
+// checks' zero registers and branches were a third of the backward pass's instructions). COLS_SINGLE: rows begin
+// anywhere: a stage takes the 16-byte chunks that hold its row (the bytes behind the tensor's end as zeros), a thread
+// owns single columns blockDim.x apart, and a barrier stands between the copies and the reads.
+enum : int { COLS_SINGLE = 0, COLS_VECTORS = 1, COLS_EXACT = 2 };
+constexpr int NORM_STAGES = 3, NORM_RING_THREADS = 512;   // 512 threads an SM leave 128 registers each
+
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void *gmem, int bytes = 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
+}
+
+template <typename XT, int N, int COLS>
+struct NormColumns {
+    static constexpr bool VEC = COLS != COLS_SINGLE;
+    static constexpr int C = 16 / static_cast<int>(sizeof(XT));   // elements of 16 bytes
+    static constexpr int V = VEC ? C : 1;
+    static constexpr int VPT = N / V;                             // vectors (single columns) of a thread
+    int K, nt, tid;
+    __device__ __forceinline__ explicit NormColumns(int k) : K(k), nt(blockDim.x), tid(threadIdx.x) {}
+
+    // elements between two rows of the ring
+    static __host__ __device__ __forceinline__ int pitch(int K) { return VEC ? K : (K + 2 * C - 2) / C * C; }
+    // where a row that starts at element `at` of its tensor begins within its place
+    __device__ __forceinline__ int offset(size_t at) const { return VEC ? 0 : static_cast<int>(at % C); }
+
+    // one row, which starts at element `at` of a tensor of `total`, into its place of the ring
+    __device__ __forceinline__ void fetch(XT *slot, const XT *x, size_t at, size_t total) const {
+        const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(slot));
+        if constexpr (VEC) {
 #pragma unroll
-                for (int o = 64 / V; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                if (i < nv) {
-                    const float sc = scale_of(m);
-                    uint8_t *q = p.q + static_cast<size_t>(row) * K + static_cast<size_t>(i) * V;
-                    if constexpr (V == 8)
-                        *reinterpret_cast<uint2 *>(q) = quant8(f[j], sc);
-                    else
-                        *reinterpret_cast<uint32_t *>(q) = quant4(f[j], sc);
-                    const int per = 128 / V;
-                    if (i % per == 0) p.sfa[static_cast<size_t>(i / per) * p.ld + row] = sc;
+            for (int j = 0; j < VPT; ++j) {
+                const int i = (j * nt + tid) * V;
+                if (COLS == COLS_EXACT || i < K) cp_async16(s + i * static_cast<int>(sizeof(XT)), x + at + i);
+            }
+        } else {
+            const size_t first = at / C * C;
+            for (int i = tid * C; first + i < at + K; i += nt * C) {
+                const size_t left = (total - first - i) * sizeof(XT);
+                cp_async16(s + i * static_cast<int>(sizeof(XT)), x + first + i, left < 16 ? static_cast<int>(left) : 16);
+            }
+        }
+    }
+    // the thread's columns of a row, 0 where it has none
+    template <typename T>
+    __device__ __forceinline__ void load(const T *row, Pair (&f)[N / 2]) const {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int i = (j * nt + tid) * V;
+                if (COLS == COLS_EXACT || i < K) {
+                    load_pairs<T, V>(row + i, f + j * (V / 2));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V / 2; ++e) f[j * (V / 2) + e] = pair(0.f, 0.f);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) {
+                const int i = 2 * e * nt + tid, i2 = i + nt;
+                f[e] = pair(i < K ? static_cast<float>(row[i]) : 0.f, i2 < K ? static_cast<float>(row[i2]) : 0.f);
+            }
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T *row, const Pair (&f)[N / 2]) const {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int i = (j * nt + tid) * V;
+                if (COLS == COLS_EXACT || i < K) store_pairs<T, V>(row + i, f + j * (V / 2));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) {
+                const int i = 2 * e * nt + tid, i2 = i + nt;
+                const float2 h = halves(f[e]);
+                if (i < K) store_vec<T, 1>(row + i, &h.x);
+                if (i2 < K) store_vec<T, 1>(row + i2, &h.y);
+            }
+        }
+    }
+    // sum over the thread's columns of (f - mu)^2
+    __device__ __forceinline__ float squares(const Pair (&f)[N / 2], float mu) const {
+        const Pair c = pair(-mu, -mu);
+        if constexpr (VEC) {
+            Pair q = pair(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if (COLS == COLS_EXACT || (j * nt + tid) * V < K) {
+#pragma unroll
+                    for (int e = 0; e < V / 2; ++e) {
+                        const Pair d = f[j * (V / 2) + e] + c;
+                        q = fma2(d, d, q);
+                    }
+                }
+            const float2 h = halves(q);
+            return h.x + h.y;
+        } else {
+            float q = 0.f;
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) {
+                const int i = 2 * e * nt + tid;
+                const float2 h = halves(f[e] + c);
+                if (i < K) q = fmaf(h.x, h.x, q);
+                if (i + nt < K) q = fmaf(h.y, h.y, q);
+            }
+            return q;
+        }
+    }
+    // columns that warp `w` of the team owns
+    __device__ __forceinline__ int count(int w) const {
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) n += max(0, min(32 * V, K - (j * nt + w * 32) * V));
+        return n;
+    }
+};
+
+// Waits for the stage that is read next and refills the one that was read last. With VEC a thread's own copies
+// are all it reads; otherwise all threads' copies must have come, and all must have left the last stage.
+template <bool VEC, typename F>
+__device__ __forceinline__ void ring_step(F refill) {
+    if constexpr (VEC) {
+        refill();
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(NORM_STAGES - 1) : "memory");
+    } else {
+        asm volatile("cp.async.wait_group %0;" ::"n"(NORM_STAGES - 2) : "memory");
+        if (blockDim.x == 32) __syncwarp();
+        else __syncthreads();
+        refill();
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+}
+
+// The mean square is taken about the warp's own mean and moved to the row's mean afterwards (as exact
+// as about the row's mean), so the R rows cost one barrier.
+template <typename XT, typename WT, int N, int R, int COLS>
+__global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_ring_kernel(const __grid_constant__ NormParams p) {
+    using Cols = NormColumns<XT, N, COLS>;
+    constexpr bool VEC = Cols::VEC;
+    extern __shared__ __align__(16) unsigned char s_norm[];
+    __shared__ float2 s_red[2][R][32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int K = p.K, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, nw = nt >> 5;
+    const int step = gridDim.x * blockDim.y;
+    const size_t total = static_cast<size_t>(p.T) * K;
+    const int pitch = Cols::pitch(K);
+    const Cols cols(K);
+    const XT *x = static_cast<const XT *>(p.x);
+    XT *ring = reinterpret_cast<XT *>(s_norm) + static_cast<size_t>(threadIdx.y) * NORM_STAGES * R * pitch;
+    constexpr bool KEEP = N <= 16;   // w and b in registers, or read again (from L1) for every row
+    Pair w[N / 2], b[N / 2];
+    const auto parameters = [&] {
+        if (p.w) {
+            cols.load(static_cast<const WT *>(p.w), w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) w[e] = pair(1.f, 1.f);
+        }
+        if (p.b) {
+            cols.load(static_cast<const WT *>(p.b), b);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) b[e] = pair(0.f, 0.f);
+        }
+    };
+    if constexpr (KEEP) parameters();
+    const int count = cols.count(tid >> 5), count_of_lane = lane < nw ? cols.count(lane) : 0;
+    const float inv_count = count ? 1.f / static_cast<float>(count) : 0.f, inv_k = 1.f / static_cast<float>(K);
+    const auto fetch = [&](int first, int stage) {
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            if (first + q * step < p.T)
+                cols.fetch(ring + (stage * R + q) * pitch, x, static_cast<size_t>(first + q * step) * K, total);
+    };
+    int row = blockIdx.x * blockDim.y + threadIdx.y;   // T <= 2^30: no sum below overflows
+#pragma unroll
+    for (int s = 0; s + 1 < NORM_STAGES; ++s) {
+        fetch(row + s * R * step, s);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int stage = 0;
+    for (int n = 0; row < p.T; ++n, row += R * step) {
+        ring_step<VEC>([&] { fetch(row + (NORM_STAGES - 1) * R * step, stage == 0 ? NORM_STAGES - 1 : stage - 1); });
+        Pair f[R][N / 2];
+        float mu[R], m2[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            mu[q] = m2[q] = 0.f;
+            const size_t at = static_cast<size_t>(row + q * step) * K;
+            if (row + q * step < p.T) {
+                cols.load(ring + (stage * R + q) * pitch + cols.offset(at), f[q]);
+                if (!p.rms) {
+                    Pair s = f[q][0];
+#pragma unroll
+                    for (int e = 1; e < N / 2; ++e) s = s + f[q][e];
+                    const float2 h = halves(s);
+                    mu[q] = h.x + h.y;
+                }
+            }
+        }
+        stage = stage + 1 == NORM_STAGES ? 0 : stage + 1;
+        if (!p.rms) {   // the warp's means
+            if constexpr (R == 2) {
+                const float2 s = warp_sum2(mu[0], mu[1]);
+                mu[0] = s.x * inv_count;
+                mu[1] = s.y * inv_count;
+            } else {
+                mu[0] = warp_sum(mu[0]) * inv_count;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            if (row + q * step < p.T) m2[q] = cols.squares(f[q], mu[q]);
+        if constexpr (R == 2) {
+            const float2 s = warp_sum2(m2[0], m2[1]);
+            m2[0] = s.x;
+            m2[1] = s.y;
+        } else {
+            m2[0] = warp_sum(m2[0]);
+        }
+        if (nt > 32) {
+            if (lane < R) s_red[n & 1][lane][tid >> 5] = make_float2(R == 2 && lane ? mu[R - 1] : mu[0], R == 2 && lane ? m2[R - 1] : m2[0]);
+            __syncthreads();   // the other half of s_red is free: all have left the last rows' sums
+            const float c = static_cast<float>(count_of_lane);
+            float2 v[R];
+            float a[R];
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                v[q] = lane < nw ? s_red[n & 1][q][lane] : make_float2(0.f, 0.f);
+                a[q] = v[q].x * c;
+            }
+            if (!p.rms) {
+                const float2 s = R == 2 ? warp_sum2(a[0], a[R - 1]) : make_float2(warp_sum(a[0]), 0.f);
+                mu[0] = s.x * inv_k;
+                if (R == 2) mu[R - 1] = s.y * inv_k;
+            }
+#pragma unroll
+            for (int q = 0; q < R; ++q) a[q] = p.rms ? v[q].y : fmaf(c * (v[q].x - mu[q]), v[q].x - mu[q], v[q].y);
+            const float2 s = R == 2 ? warp_sum2(a[0], a[R - 1]) : make_float2(warp_sum(a[0]), 0.f);
+            m2[0] = s.x;
+            if (R == 2) m2[R - 1] = s.y;
+        }
+        if constexpr (!KEEP) parameters();
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int t = row + q * step;
+            if (t >= p.T) break;   // the same for the whole team
+            const float r = 1.f / sqrtf(fmaf(m2[q], inv_k, p.eps));
+            if (tid == 0) {
+                if (p.mean) p.mean[t] = mu[q];
+                if (p.rstd) p.rstd[t] = r;
+            }
+            const Pair c = pair(-mu[q], -mu[q]), rr = pair(r, r);
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e) f[q][e] = fma2((f[q][e] + c) * rr, w[e], b[e]);
+            if (p.y) cols.store(static_cast<XT *>(p.y) + static_cast<size_t>(t) * K, f[q]);
+            if constexpr (VEC) {
+                if (p.q) {   // K % 128 == 0: the threads of a slice are all inside the row or all outside
+                    constexpr int V = Cols::V;
+#pragma unroll
+                    for (int j = 0; j < Cols::VPT; ++j) {
+                        float v[V], m = 0.f;
+#pragma unroll
+                        for (int e = 0; e < V / 2; ++e) {
+                            const float2 h = halves(f[q][j * (V / 2) + e]);
+                            v[2 * e] = h.x;
+                            v[2 * e + 1] = h.y;
+                            m = fmaxf(m, fmaxf(fabsf(h.x), fabsf(h.y)));
+                        }
+                        norm_cast<V>(p, v, m, t, j * nt + tid, K / V);
+                    }
                 }
             }
         }
@@ -203,7 +568,7 @@ struct NormBackParams {
     int T, K, parts;
 };
 
-// dx of one row per blockDim.x threads, laid out as in the forward kernel.
+// Long rows: dx of one row per blockDim.x threads, laid out as in the forward kernel.
 template <typename XT, typename WT, int V, int VPT>
 __global__ void __launch_bounds__(NORM_DX_MAX_THREADS) layer_norm_dx_kernel(const NormBackParams p) {
     __shared__ float s_red[2][32];
@@ -248,7 +613,8 @@ __global__ void __launch_bounds__(NORM_DX_MAX_THREADS) layer_norm_dx_kernel(cons
     }
 }
 
-// Column sums over one part of the rows: block (32, 8), a thread a column, 8 rows at a time;
+// Rows too long for the kernel below (their ring does not fit): the column sums over one part of the rows.
+// Block (32, 8), a thread a column, 8 rows at a time;
 // grid (ceil(K/32), parts).
 template <typename XT>
 __global__ void __launch_bounds__(256) layer_norm_dwdb_kernel(const NormBackParams p) {
@@ -279,19 +645,179 @@ __global__ void __launch_bounds__(256) layer_norm_dwdb_kernel(const NormBackPara
     }
 }
 
-// dw and db from the parts, added in the parts' order: a thread a column.
-__global__ void __launch_bounds__(256) layer_norm_parts_kernel(const NormBackParams p) {
+// dx, and the sums of dw and db, in one pass over dy and x: HBM-bound (three tensors of T·K). Teams, columns
+// and the ring are those of the forward kernel, with rows of x and dy side by side; a thread's columns' dw
+// and db stay in registers to the end, and R rows cost one barrier for their sums of u and u·(x - mu).
+// dx = (dy·r)·w - r·c1 - xh·(r·c2) with c1 = mean(u), c2 = r·mean(u·(x - mu)).
+// The teams' sums meet in shared memory and go to part[blockIdx.x] in a fixed order.
+template <typename XT, typename WT, int N, int R, int COLS>
+__global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(const __grid_constant__ NormBackParams p) {
+    using Cols = NormColumns<XT, N, COLS>;
+    constexpr bool VEC = Cols::VEC;
+    constexpr int H = N / 2;
+    extern __shared__ __align__(16) unsigned char s_norm[];
+    __shared__ float4 s_red[2][32];
     pdl_launch_dependents();
     pdl_wait();
-    const int col = blockIdx.x * 256 + threadIdx.x;
-    if (col >= p.K) return;
-    float aw = 0.f, ab = 0.f;
-    for (int i = 0; i < p.parts; ++i) {
-        aw += p.part[(static_cast<size_t>(i) * 2) * p.K + col];
-        ab += p.part[(static_cast<size_t>(i) * 2 + 1) * p.K + col];
+    const int K = p.K, nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, teams = blockDim.y;
+    const int step = gridDim.x * teams;
+    const size_t total = static_cast<size_t>(p.T) * K;
+    const int pitch = Cols::pitch(K);
+    const Cols cols(K);
+    const XT *x = static_cast<const XT *>(p.x), *dy = static_cast<const XT *>(p.dy);
+    XT *ring = reinterpret_cast<XT *>(s_norm) + static_cast<size_t>(threadIdx.y) * NORM_STAGES * R * 2 * pitch;
+    const float inv_k = 1.f / static_cast<float>(K);
+    const Pair zero = pair(0.f, 0.f);
+    constexpr bool KEEP = N <= 16;   // w in registers, or read again (from L1) for every row
+    Pair w[H], aw[H], ab[H];
+    const auto parameters = [&] {
+        if (p.w) {
+            cols.load(static_cast<const WT *>(p.w), w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < H; ++e) w[e] = pair(1.f, 1.f);
+        }
+    };
+    if constexpr (KEEP) parameters();
+#pragma unroll
+    for (int e = 0; e < H; ++e) aw[e] = ab[e] = zero;
+    const auto fetch = [&](int first, int stage) {
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+            if (first + q * step < p.T) {
+                const size_t at = static_cast<size_t>(first + q * step) * K;
+                cols.fetch(ring + (stage * R + q) * 2 * pitch, x, at, total);
+                cols.fetch(ring + ((stage * R + q) * 2 + 1) * pitch, dy, at, total);
+            }
+    };
+    int row = blockIdx.x * teams + threadIdx.y;   // T <= 2^30: no sum below overflows
+#pragma unroll
+    for (int s = 0; s + 1 < NORM_STAGES; ++s) {
+        fetch(row + s * R * step, s);
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    if (p.dw) p.dw[col] = aw;
-    if (p.db) p.db[col] = ab;
+    float mu[R], r[R];
+    const auto statistics = [&](int first, float (&m)[R], float (&s)[R]) {
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const bool in = first + q * step < p.T;
+            s[q] = in ? p.rstd[first + q * step] : 0.f;
+            m[q] = in && p.mean ? p.mean[first + q * step] : 0.f;
+        }
+    };
+    statistics(row, mu, r);
+    int stage = 0;
+    for (int n = 0; row < p.T; ++n, row += R * step) {
+        ring_step<VEC>([&] { fetch(row + (NORM_STAGES - 1) * R * step, stage == 0 ? NORM_STAGES - 1 : stage - 1); });
+        float mu_next[R], r_next[R];
+        statistics(row + R * step, mu_next, r_next);
+        float sums[2 * R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            sums[2 * q] = sums[2 * q + 1] = 0.f;
+            if (row + q * step < p.T) {
+                const int off = cols.offset(static_cast<size_t>(row + q * step) * K);
+                Pair fx[H], fd[H];
+                if constexpr (!KEEP) parameters();
+                cols.load(ring + (stage * R + q) * 2 * pitch + off, fx);
+                cols.load(ring + ((stage * R + q) * 2 + 1) * pitch + off, fd);
+                const Pair c = pair(-mu[q], -mu[q]);
+                Pair s1 = zero, s2 = zero;
+#pragma unroll
+                for (int e = 0; e < H; ++e) {
+                    const Pair u = fd[e] * w[e];
+                    s1 = s1 + u;
+                    s2 = fma2(u, fx[e] + c, s2);
+                }
+                const float2 h1 = halves(s1), h2 = halves(s2);
+                sums[2 * q] = h1.x + h1.y;
+                sums[2 * q + 1] = h2.x + h2.y;
+            }
+        }
+        if constexpr (R == 2) {
+            float s = warp_sum4_spread(make_float4(sums[0], sums[1], sums[2], sums[3]));
+            if (nt > 32) {
+                if (lane % 8 == 0) reinterpret_cast<float *>(&s_red[n & 1][tid >> 5])[lane / 8] = s;
+                __syncthreads();   // the other half of s_red is free: all have left the last rows' sums
+                s = warp_sum4_spread(lane < nt / 32 ? s_red[n & 1][lane] : make_float4(0.f, 0.f, 0.f, 0.f));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sums[i] = __shfl_sync(0xFFFFFFFFu, s, 8 * i);
+        } else {
+            float2 s = warp_sum2(sums[0], sums[1]);
+            if (nt > 32) {
+                if (lane == 0) s_red[n & 1][tid >> 5] = make_float4(s.x, s.y, 0.f, 0.f);
+                __syncthreads();
+                const float4 v = lane < nt / 32 ? s_red[n & 1][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+                s = warp_sum2(v.x, v.y);
+            }
+            sums[0] = s.x;
+            sums[1] = s.y;
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            if (row + q * step < p.T) {
+                const size_t at = static_cast<size_t>(row + q * step) * K;
+                Pair fx[H], fd[H];   // read again: they need not live across the sums
+                if constexpr (!KEEP) parameters();
+                cols.load(ring + (stage * R + q) * 2 * pitch + cols.offset(at), fx);
+                cols.load(ring + ((stage * R + q) * 2 + 1) * pitch + cols.offset(at), fd);
+                const float rq = r[q], b0 = p.mean ? -rq * (sums[2 * q] * inv_k) : 0.f;
+                const float a0 = -rq * (rq * (sums[2 * q + 1] * inv_k));   // -r·c2, c2 = r·mean(u·d)
+                const Pair c = pair(-mu[q], -mu[q]), rr = pair(rq, rq), pa = pair(a0, a0), pb = pair(b0, b0);
+#pragma unroll
+                for (int e = 0; e < H; ++e) {
+                    const Pair xh = (fx[e] + c) * rr;
+                    ab[e] = ab[e] + fd[e];
+                    aw[e] = fma2(fd[e], xh, aw[e]);
+                    fx[e] = fma2(fd[e] * rr, w[e], fma2(xh, pa, pb));
+                }
+                cols.store(static_cast<XT *>(p.dx) + at, fx);
+            }
+            mu[q] = mu_next[q];
+            r[q] = r_next[q];
+        }
+        stage = stage + 1 == NORM_STAGES ? 0 : stage + 1;
+    }
+    if (!p.part) return;
+    float *part = p.part + static_cast<size_t>(blockIdx.x) * 2 * K;
+    float *out = teams == 1 ? part : reinterpret_cast<float *>(s_norm) + threadIdx.y * 2 * K;
+    if (teams > 1) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();   // the ring becomes the teams' sums [teams][2][K]
+    }
+    cols.store(out, aw);
+    cols.store(out + K, ab);
+    if (teams == 1) return;
+    __syncthreads();
+    for (int i = threadIdx.y * nt + tid; i < 2 * K; i += teams * nt) {
+        float a = 0.f;
+        for (int m = 0; m < teams; ++m) a += reinterpret_cast<const float *>(s_norm)[m * 2 * K + i];
+        part[i] = a;
+    }
+}
+
+// dw and db from the parts: block (32, 16), a column a thread; thread row y adds the parts y, y + 16, ...,
+// and the 16 sums are added in their order. Grid (ceil(K/32), 2).
+__global__ void __launch_bounds__(512) layer_norm_parts_kernel(const __grid_constant__ NormBackParams p) {
+    __shared__ float s_sum[16][33];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int col = blockIdx.x * 32 + threadIdx.x;
+    float *out = blockIdx.y ? p.db : p.dw;
+    float a = 0.f;
+    if (out && col < p.K) {
+        const float *part = p.part + static_cast<size_t>(blockIdx.y) * p.K + col;
+#pragma unroll 8
+        for (int i = threadIdx.y; i < p.parts; i += 16) a += part[static_cast<size_t>(i) * 2 * p.K];
+    }
+    s_sum[threadIdx.y][threadIdx.x] = a;
+    __syncthreads();
+    if (threadIdx.y == 0 && out && col < p.K) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) a += s_sum[i][threadIdx.x];
+        out[col] = a;
+    }
 }
 
 }  // namespace dg

@@ -45,8 +45,8 @@ def cuda(t):
     return None if t is None else t.cuda()
 
 
-SHAPES = [(1, 1), (3, 2), (2, 7), (9, 64), (5, 129), (17, 1000), (300, 1001), (1, 7168), (33, 2048), (311, 7168),
-          (7, 4097), (2, 8191), (600, 24), (3, 16384), (2, 20001), (2, 32768), (299, 260)]
+SHAPES = [(1, 1), (3, 2), (2, 7), (9, 64), (5, 129), (17, 1000), (300, 1001), (777, 1001), (1, 7168), (33, 2048), (311, 7168),
+          (7, 4097), (2, 8191), (600, 24), (1000, 128), (333, 256), (700, 512), (3, 16384), (310, 16384), (301, 12296), (2, 20001), (2, 32768), (299, 260)]
 
 
 @pytest.mark.parametrize("T,K", SHAPES)
