@@ -332,15 +332,11 @@ DG_API dg_status dg_moe_route_backward(const float *grad_weights, const void *lo
  *   masked: expert g's rows are g·M_max, g·M_max + 1, ...; masked_m int32 [G], their number.
  * A pair whose row would lie outside M_sum (or at or behind M_max) gets row -1 and sets the device
  * error word; ks and masked_m are clamped.
- *   workspace  dg_moe_layout_workspace(T, k, G) bytes of device memory (0 for up to 2048 pairs),
- *              16-byte aligned, for this call alone until its work on the stream is done.
  * Limits: G <= 1024, T·k <= 2^30, G·M_max < 2^31. */
 DG_API dg_status dg_moe_layout_contiguous(const int32_t *ids, int32_t *dst_rows, int32_t *grouped_layout, int32_t *ks,
-                                          void *workspace, long long workspace_bytes, int T, int k, int G, int M_sum,
-                                          void *stream);
-DG_API dg_status dg_moe_layout_masked(const int32_t *ids, int32_t *dst_rows, int32_t *masked_m, void *workspace,
-                                      long long workspace_bytes, int T, int k, int G, int M_max, void *stream);
-DG_API long long dg_moe_layout_workspace(int T, int k, int G);
+                                          int T, int k, int G, int M_sum, void *stream);
+DG_API dg_status dg_moe_layout_masked(const int32_t *ids, int32_t *dst_rows, int32_t *masked_m, int T, int k, int G,
+                                      int M_max, void *stream);
 
 /* dg_cast_fp8_per_token_scatter for k rows per token and both grouped layouts: token t is
  * quantised once and written to the rows dst_rows[t][0..k-1] (int32 [T,k]; negative: none) of G

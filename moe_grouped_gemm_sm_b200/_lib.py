@@ -71,9 +71,8 @@ def load():
             "dg_layer_norm_backward_workspace": [I, I],
             "dg_moe_route": [P, P, P, P, I, I, I, I, I, I, I, I, F, I, P],
             "dg_moe_route_backward": [P, P, P, P, I, I, I, I, I, F, I, P],
-            "dg_moe_layout_contiguous": [P, P, P, P, P, Q, I, I, I, I, P],
-            "dg_moe_layout_masked": [P, P, P, P, Q, I, I, I, I, P],
-            "dg_moe_layout_workspace": [I, I, I],
+            "dg_moe_layout_contiguous": [P, P, P, P, I, I, I, I, P],
+            "dg_moe_layout_masked": [P, P, P, I, I, I, I, P],
             "dg_cast_fp8_per_token_scatter_topk": [P, P, P, P, I, I, I, I, I, P],
             "dg_moe_combine": [P, P, P, P, P, I, I, I, I, P],
             "dg_moe_combine_backward": [P, P, P, P, P, P, P, I, I, I, I, P],
@@ -85,8 +84,7 @@ def load():
             f = getattr(L, name)
             f.argtypes = args
             f.restype = {"dg_status_string": ctypes.c_char_p, "dg_last_kernel": ctypes.c_char_p,
-                         "dg_allocated_bytes": Q, "dg_moe_layout_workspace": Q,
-                         "dg_layer_norm_backward_workspace": Q}.get(name, I)
+                         "dg_allocated_bytes": Q, "dg_layer_norm_backward_workspace": Q}.get(name, I)
         _lib = L
     return _lib
 
@@ -212,18 +210,13 @@ def dg_moe_route_backward(grad_weights, logits, ids, grad_logits, T, E, k, score
           scale, dtype, _stream(stream))
 
 
-def dg_moe_layout_workspace(T: int, k: int, G: int) -> int:
-    return load().dg_moe_layout_workspace(T, k, G)
+def dg_moe_layout_contiguous(ids, dst_rows, grouped_layout, ks, T, k, G, M_sum, stream=None):
+    _call("dg_moe_layout_contiguous", _ptr(ids), _ptr(dst_rows), _ptr(grouped_layout), _ptr(ks), T, k, G, M_sum,
+          _stream(stream))
 
 
-def dg_moe_layout_contiguous(ids, dst_rows, grouped_layout, ks, workspace, workspace_bytes, T, k, G, M_sum, stream=None):
-    _call("dg_moe_layout_contiguous", _ptr(ids), _ptr(dst_rows), _ptr(grouped_layout), _ptr(ks), _ptr(workspace),
-          workspace_bytes, T, k, G, M_sum, _stream(stream))
-
-
-def dg_moe_layout_masked(ids, dst_rows, masked_m, workspace, workspace_bytes, T, k, G, M_max, stream=None):
-    _call("dg_moe_layout_masked", _ptr(ids), _ptr(dst_rows), _ptr(masked_m), _ptr(workspace), workspace_bytes, T, k, G,
-          M_max, _stream(stream))
+def dg_moe_layout_masked(ids, dst_rows, masked_m, T, k, G, M_max, stream=None):
+    _call("dg_moe_layout_masked", _ptr(ids), _ptr(dst_rows), _ptr(masked_m), T, k, G, M_max, _stream(stream))
 
 
 def dg_cast_fp8_per_token_scatter_topk(x, dst_rows, q, sfa, T, k, G, M, K, stream=None):

@@ -211,22 +211,42 @@ dg_status run_route(const dg::RouteParams &p, int sm_count, cudaStream_t st) {
     return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::route_kernel<LT, 32>, p));
 }
 
-// Pairs per block of the layout kernels, a multiple of 256.
-int layout_chunk(int n) {
-    if (n <= dg::LAYOUT_CHUNK) return dg::LAYOUT_CHUNK;
-    const int c = (n + dg::LAYOUT_MAX_CHUNKS - 1) / dg::LAYOUT_MAX_CHUNKS;
-    return std::max(dg::LAYOUT_CHUNK, (c + 255) / 256 * 256);
-}
-
 bool layout_sizes_ok(int T, int k, int G) {
     return T >= 0 && k > 0 && G > 0 && G <= dg::LAYOUT_MAX_G && static_cast<long long>(T) * k <= (1LL << 30);
 }
 
+// 2^BITS >= G. The counts of [warps][G] stay within 48 KB of shared memory; a second block of the cluster comes with
+// more than 64 pairs a warp (its barriers cost about as much as two rounds of 32 pairs). Clusters of 16 where
+// the device can hold one, else of 8.
+template <bool MASKED, int BITS>
+dg_status launch_layout(dg::LayoutParams p, cudaStream_t st) {
+    const auto kernel = dg::layout_kernel<MASKED, BITS>;
+    const int warps = p.G <= 256 ? 32 : (p.G <= 512 ? 16 : 8);
+    const size_t smem = static_cast<size_t>(p.G) * 4 * (3 + warps);
+    static std::atomic<int> most[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return DG_ERR_CUDA;
+    if (most[dev].load() == 0) {
+        int n = 0;
+        Launch ln(dim3(16, 1, 1), dim3(1024, 1, 1), 46 << 10, st, 16);   // the most that any G takes: 11·4·1024
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &ln.cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        most[dev].store(n > 0 ? 16 : 8);
+    }
+    int blocks = 1;
+    while (blocks < most[dev].load() && p.n > blocks * warps * 64) blocks *= 2;
+    const int all = blocks * warps;
+    p.per_warp = static_cast<int>(std::max(1LL, (static_cast<long long>(p.n) + all * 32 - 1) / (all * 32))) * 32;
+    Launch ln(dim3(static_cast<unsigned>(blocks), 1, 1), dim3(static_cast<unsigned>(32 * warps), 1, 1), smem, st, blocks);
+    return from_cuda(cudaLaunchKernelEx(&ln.cfg, kernel, p));
+}
+
 template <bool MASKED>
-dg_status run_layout(const int32_t *ids, int32_t *dst_rows, int32_t *grouped_layout, int32_t *counts, void *workspace,
-                     long long workspace_bytes, int T, int k, int G, int M, cudaStream_t st) {
-    const long long need = dg_moe_layout_workspace(T, k, G);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return DG_ERR_INVALID_ARG;
+dg_status run_layout(const int32_t *ids, int32_t *dst_rows, int32_t *grouped_layout, int32_t *counts, int T, int k, int G,
+                     int M, cudaStream_t st) {
     const DeviceInfo *di = nullptr;
     dg_status s = device_info(&di);
     if (s != DG_OK) return s;
@@ -235,21 +255,13 @@ dg_status run_layout(const int32_t *ids, int32_t *dst_rows, int32_t *grouped_lay
     p.dst_rows = dst_rows;
     p.grouped_layout = grouped_layout;
     p.counts = counts;
-    p.hist = static_cast<int32_t *>(workspace);
     p.err = di->err;
     p.n = T * k;
     p.G = G;
     p.M = M;
-    p.chunk = layout_chunk(p.n);
-    p.chunks = std::max(1, static_cast<int>((static_cast<long long>(p.n) + p.chunk - 1) / p.chunk));
-    const dim3 grid(static_cast<unsigned>(p.chunks), 1, 1), block(dg::LAYOUT_THREADS, 1, 1);
-    if (p.chunks > 1) {
-        Launch ln(grid, block, static_cast<size_t>(G) * 4, st);
-        s = from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::layout_count_kernel, p));
-        if (s != DG_OK) return s;
-    }
-    Launch ln(grid, block, static_cast<size_t>(G) * 4 * (2 + dg::LAYOUT_WARPS), st);
-    return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::layout_place_kernel<MASKED>, p));
+    if (G <= 32) return launch_layout<MASKED, 5>(p, st);
+    if (G <= 256) return launch_layout<MASKED, 8>(p, st);
+    return launch_layout<MASKED, 10>(p, st);
 }
 
 }  // namespace
@@ -397,32 +409,22 @@ dg_status dg_moe_route_backward(const float *grad_weights, const void *logits, c
                                       : cudaLaunchKernelEx(&ln.cfg, dg::route_backward_kernel<float>, p));
 }
 
-long long dg_moe_layout_workspace(int T, int k, int G) {
-    if (!layout_sizes_ok(T, k, G)) return 0;
-    const int n = T * k, chunk = layout_chunk(n);
-    const long long chunks = (static_cast<long long>(n) + chunk - 1) / chunk;
-    return chunks > 1 ? chunks * G * 4 : 0;
-}
-
-dg_status dg_moe_layout_contiguous(const int32_t *ids, int32_t *dst_rows, int32_t *grouped_layout, int32_t *ks,
-                                   void *workspace, long long workspace_bytes, int T, int k, int G, int M_sum,
-                                   void *stream) {
-    if ((T > 0 && (!ids || !dst_rows)) || (M_sum > 0 && !grouped_layout) || !layout_sizes_ok(T, k, G) || M_sum < 0 || M_sum % 128 != 0)
+dg_status dg_moe_layout_contiguous(const int32_t *ids, int32_t *dst_rows, int32_t *grouped_layout, int32_t *ks, int T, int k,
+                                   int G, int M_sum, void *stream) {
+    if ((T > 0 && (!ids || !dst_rows)) || (M_sum > 0 && !grouped_layout) || !layout_sizes_ok(T, k, G) || M_sum < 0 ||
+        M_sum % 128 != 0)
         return DG_ERR_INVALID_ARG;
-    if (!aligned16(ids) || !aligned16(dst_rows) || !aligned16(grouped_layout) || !aligned16(ks) || !aligned16(workspace))
-        return DG_ERR_ALIGNMENT;
-    return run_layout<false>(ids, dst_rows, grouped_layout, ks, workspace, workspace_bytes, T, k, G, M_sum,
-                             static_cast<cudaStream_t>(stream));
+    if (!aligned16(ids) || !aligned16(dst_rows) || !aligned16(grouped_layout) || !aligned16(ks)) return DG_ERR_ALIGNMENT;
+    return run_layout<false>(ids, dst_rows, grouped_layout, ks, T, k, G, M_sum, static_cast<cudaStream_t>(stream));
 }
 
-dg_status dg_moe_layout_masked(const int32_t *ids, int32_t *dst_rows, int32_t *masked_m, void *workspace,
-                               long long workspace_bytes, int T, int k, int G, int M_max, void *stream) {
+dg_status dg_moe_layout_masked(const int32_t *ids, int32_t *dst_rows, int32_t *masked_m, int T, int k, int G, int M_max,
+                               void *stream) {
     if ((T > 0 && (!ids || !dst_rows)) || !masked_m || !layout_sizes_ok(T, k, G) || M_max < 0 ||
         static_cast<long long>(G) * M_max >= (1LL << 31))
         return DG_ERR_INVALID_ARG;
-    if (!aligned16(ids) || !aligned16(dst_rows) || !aligned16(masked_m) || !aligned16(workspace)) return DG_ERR_ALIGNMENT;
-    return run_layout<true>(ids, dst_rows, nullptr, masked_m, workspace, workspace_bytes, T, k, G, M_max,
-                            static_cast<cudaStream_t>(stream));
+    if (!aligned16(ids) || !aligned16(dst_rows) || !aligned16(masked_m)) return DG_ERR_ALIGNMENT;
+    return run_layout<true>(ids, dst_rows, nullptr, masked_m, T, k, G, M_max, static_cast<cudaStream_t>(stream));
 }
 
 dg_status dg_cast_fp8_per_token_scatter_topk(const void *x, const int32_t *dst_rows, void *q, float *sfa, int T, int k,
@@ -435,11 +437,16 @@ dg_status dg_cast_fp8_per_token_scatter_topk(const void *x, const int32_t *dst_r
     const DeviceInfo *di = nullptr;
     dg_status s = device_info(&di);
     if (s != DG_OK) return s;
-    const long long blocks = (static_cast<long long>(T) * (K / 128) + 15) / 16;
-    if (blocks >= (1LL << 31)) return DG_ERR_INVALID_ARG;
-    Launch ln(dim3(static_cast<unsigned>(blocks), 1, 1), dim3(256, 1, 1), 0, static_cast<cudaStream_t>(stream));
+    // a thread takes 16 elements; few tokens are cut along K until there are two blocks per SM
+    int threads = std::min(dg::SCATTER_THREADS, (K / 16 + 31) / 32 * 32);
+    while (static_cast<long long>(T) * ((K / 16 + threads - 1) / threads) < 2LL * di->sm_count && threads > 64)
+        threads = (threads / 2 + 31) / 32 * 32;
+    const int parts = T < 2 * di->sm_count ? (K / 16 + threads - 1) / threads : 1;
+    if (parts > 65535) return DG_ERR_INVALID_ARG;
+    Launch ln(dim3(static_cast<unsigned>(T), static_cast<unsigned>(parts), 1), dim3(static_cast<unsigned>(threads), 1, 1), 0,
+              static_cast<cudaStream_t>(stream));
     return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::cast_scatter_topk_kernel, static_cast<const __nv_bfloat16 *>(x),
-                                        dst_rows, static_cast<uint8_t *>(q), sfa, T, k, K, M, pad4(M),
+                                        dst_rows, static_cast<uint8_t *>(q), sfa, k, K, M, pad4(M),
                                         static_cast<long long>(G) * M, di->err));
 }
 

@@ -337,11 +337,6 @@ def moe_route_backward(grad_weights, logits, ids, score="softmax", renorm=True, 
     return g
 
 
-def _layout_workspace(T, k, G, device):
-    need = _lib.dg_moe_layout_workspace(T, k, G)
-    return (torch.empty(need, dtype=torch.uint8, device=device) if need else None), need
-
-
 def moe_layout_contiguous(ids, G, M_sum=None, stream=None):
     """Rows of the contiguous layout for expert ids int32 [T,k] (ids outside [0,G) are dropped):
     (dst_rows int32 [T,k], grouped_layout int32 [M_sum], ks int32 [G]). ks are the experts' padded row
@@ -353,8 +348,7 @@ def moe_layout_contiguous(ids, G, M_sum=None, stream=None):
         dst = torch.empty_like(ids)
         layout = ids.new_empty(M_sum)
         ks = ids.new_empty(G)
-        ws, need = _layout_workspace(T, k, G, ids.device)
-        _lib.dg_moe_layout_contiguous(ids, dst, layout, ks, ws, need, T, k, G, M_sum)
+        _lib.dg_moe_layout_contiguous(ids, dst, layout, ks, T, k, G, M_sum)
     return dst, layout, ks
 
 
@@ -365,8 +359,7 @@ def moe_layout_masked(ids, G, M_max, stream=None):
     with _on(ids.get_device(), stream):
         dst = torch.empty_like(ids)
         masked_m = ids.new_empty(G)
-        ws, need = _layout_workspace(T, k, G, ids.device)
-        _lib.dg_moe_layout_masked(ids, dst, masked_m, ws, need, T, k, G, M_max)
+        _lib.dg_moe_layout_masked(ids, dst, masked_m, T, k, G, M_max)
     return dst, masked_m
 
 

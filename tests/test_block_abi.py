@@ -63,25 +63,22 @@ def test_route_backward(lib, change, status):
 
 
 def test_layouts(lib):
-    def contiguous(ids=P, dst=P, layout=P, ks=P, ws=P, wb=1 << 30, T=4, k=2, G=8, M=1024):
-        return lib.dg_moe_layout_contiguous(ids, dst, layout, ks, ws, wb, T, k, G, M, None)
+    def contiguous(ids=P, dst=P, layout=P, ks=P, T=4, k=2, G=8, M=1024):
+        return lib.dg_moe_layout_contiguous(ids, dst, layout, ks, T, k, G, M, None)
 
-    def masked(ids=P, dst=P, mm=P, ws=P, wb=1 << 30, T=4, k=2, G=8, M=256):
-        return lib.dg_moe_layout_masked(ids, dst, mm, ws, wb, T, k, G, M, None)
+    def masked(ids=P, dst=P, mm=P, T=4, k=2, G=8, M=256):
+        return lib.dg_moe_layout_masked(ids, dst, mm, T, k, G, M, None)
 
     for bad in (dict(ids=None), dict(dst=None), dict(layout=None), dict(T=-1), dict(k=0), dict(G=0), dict(G=1025),
-                dict(M=100), dict(M=-128), dict(T=1 << 30), dict(T=4096, ws=None), dict(T=4096, wb=8)):
+                dict(M=100), dict(M=-128), dict(T=1 << 30)):
         assert contiguous(**bad) == BAD, bad
     for bad in (dict(ids=None), dict(dst=None), dict(mm=None), dict(T=-1), dict(k=0), dict(G=0), dict(G=1025), dict(M=-1),
-                dict(G=1024, M=1 << 21), dict(T=4096, ws=None), dict(T=4096, wb=8)):
+                dict(G=1024, M=1 << 21)):
         assert masked(**bad) == BAD, bad
-    assert contiguous(layout=P + 4) == ALIGN and contiguous(ws=P + 4) == ALIGN and masked(ids=P + 4) == ALIGN
+    assert contiguous(layout=P + 4) == ALIGN and contiguous(ks=P + 4) == ALIGN and masked(ids=P + 4) == ALIGN
 
 
 def test_workspace_sizes(lib):
-    assert _lib.dg_moe_layout_workspace(1024, 2, 256) == 0
-    assert _lib.dg_moe_layout_workspace(-1, 2, 256) == 0 and _lib.dg_moe_layout_workspace(4, 2, 5000) == 0
-    assert 0 < _lib.dg_moe_layout_workspace(1 << 16, 8, 256) <= 1 << 22
     assert _lib.dg_layer_norm_backward_workspace(0, 128) == 0
     assert _lib.dg_layer_norm_backward_workspace(1, 128) > 0
     assert _lib.dg_layer_norm_backward_workspace(8192, 7168) <= 64 << 20

@@ -94,7 +94,8 @@ def test_layouts_that_are_too_small(T, k, G):
 
 
 @pytest.mark.parametrize("T,k,G,M,K", [(1, 1, 1, 128, 128), (7, 8, 1, 1024, 384), (200, 3, 1, 1152, 7168), (64, 8, 16, 50, 640),
-                                       (33, 2, 5, 33, 256), (1500, 4, 1, 6272, 1024), (1, 32, 2, 32, 2048)])
+                                       (33, 2, 5, 33, 256), (1500, 4, 1, 6272, 1024), (1, 32, 2, 32, 2048), (2, 100, 1, 512, 256),
+                                       (3, 7, 4, 9, 17024), (400, 8, 1, 3584, 2048)])
 def test_dispatch_cast(oracle, T, k, G, M, K):
     """Bit for bit the per-token cast in the rows of the pairs; every other row as it was."""
     x = synth.normal_bf16(T + K, (T, K))
