@@ -531,34 +531,34 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS, EPL <= 8 ? 8 : 1) route_kern
 //   sigmoid:          dx_j = scale·g_j·s_j·(1 - s_j);
 //   softmax:          dx_e = s_e·(scale·g_e - sum_i scale·g_i·s_i) for every e (g_e = 0 unless chosen).
 // A choice that stands twice in a row adds both gradients.
+// The row is first written without the choices (zeros in 16-byte stores, or the softmax term), then each choice's
+// lane writes its own element: only the k chosen logits are read, except for softmax without renorm.
 template <typename LT>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS) route_backward_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * ROUTE_WARPS) route_backward_kernel(const __grid_constant__ RouteParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * ROUTE_WARPS + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, E = p.E;
+    const long long t = static_cast<long long>(blockIdx.x) * ROUTE_WARPS + (threadIdx.x >> 5);
     if (t >= p.T) return;
-    const LT *row = static_cast<const LT *>(p.logits) + static_cast<size_t>(t) * p.E;
-    LT *out = static_cast<LT *>(p.grad_logits) + static_cast<size_t>(t) * p.E;
+    const LT *row = static_cast<const LT *>(p.logits) + static_cast<size_t>(t) * E;
+    LT *out = static_cast<LT *>(p.grad_logits) + static_cast<size_t>(t) * E;
     int id = -1;
     float g = 0.f, x = 0.f;
     if (lane < p.k) {
         id = p.ids[static_cast<size_t>(t) * p.k + lane];
-        if (id >= p.E) {
+        g = p.grad_w[static_cast<size_t>(t) * p.k + lane];
+        if (id >= E) {
             report_error(p.err, ERR_DATA);
             id = -1;
         }
-        if (id >= 0) {
-            g = p.grad_w[static_cast<size_t>(t) * p.k + lane];
-            x = fminf(static_cast<float>(row[id]), CUDART_MAX_NORMAL_F);
-        }
+        if (id >= 0) x = fminf(static_cast<float>(row[id]), CUDART_MAX_NORMAL_F);
     }
     const bool in = id >= 0, full = p.score == SCORE_SOFTMAX && !p.renorm;
     float mx = -CUDART_INF_F, sum = 0.f;
     if (full) {
-        for (int e = lane; e < p.E; e += 32) mx = fmaxf(mx, route_logit(static_cast<float>(row[e]), nullptr));
-        mx = warp_max(mx);
-        for (int e = lane; e < p.E; e += 32) {
+        for (int e = lane; e < E; e += 32) mx = fmaxf(mx, route_logit(static_cast<float>(row[e]), nullptr));
+        mx = redux_max(mx);
+        for (int e = lane; e < E; e += 32) {
             const float v = route_logit(static_cast<float>(row[e]), nullptr);
             if (v > -CUDART_INF_F) sum += expf(v - mx);
         }
@@ -568,22 +568,34 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_backward_kernel(const 
     const float total = warp_sum(in ? g * o : 0.f);
     float dx = in ? p.scale * (o * (p.renorm ? g - total : g)) : 0.f;
     if (in && p.score == SCORE_SIGMOID) dx *= sigmoid_scaled(-x, 0.f);
-    for (int base = 0; base < p.E; base += 32) {
-        const int e = base + lane;
-        float v = 0.f;
-        for (int j = 0; j < p.k; ++j) {
-            const int idj = __shfl_sync(0xFFFFFFFFu, id, j);
-            const float dj = __shfl_sync(0xFFFFFFFFu, dx, j);
-            if (idj == e) v += dj;
+    if (full) {
+        const float c = p.scale * total / sum;
+        for (int e = lane; e < E; e += 32) {
+            const float v = route_logit(static_cast<float>(row[e]), nullptr);
+            const float d = v > -CUDART_INF_F ? -c * expf(v - mx) : 0.f;
+            store_vec<LT, 1>(out + e, &d);
         }
-        if (e < p.E) {
-            if (full) {
-                const float xe = route_logit(static_cast<float>(row[e]), nullptr);
-                if (xe > -CUDART_INF_F) v -= p.scale * (total * (expf(xe - mx) / sum));
-            }
-            store_vec<LT, 1>(out + e, &v);
-        }
+    } else if (E * sizeof(LT) % 16 == 0) {
+        for (int e = lane; e < E * static_cast<int>(sizeof(LT)) / 16; e += 32)
+            reinterpret_cast<uint4 *>(out)[e] = make_uint4(0, 0, 0, 0);
+    } else {
+        const float zero = 0.f;
+        for (int e = lane; e < E; e += 32) store_vec<LT, 1>(out + e, &zero);
     }
+    // the first lane of equal ids writes their sum
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
+    const bool first = in && __ffs(same) - 1 == lane;
+    if (__any_sync(0xFFFFFFFFu, in && !first)) {
+        float s = 0.f;
+        for (int j = 0; j < p.k; ++j) {
+            const float d = __shfl_sync(0xFFFFFFFFu, dx, j);
+            if ((same >> j) & 1u) s += d;
+        }
+        dx = s;
+    }
+    if (full) dx -= p.scale * (total * o);
+    __syncwarp();
+    if (first) store_vec<LT, 1>(out + id, &dx);
 }
 
 }  // namespace dg
