@@ -90,9 +90,7 @@ def load():
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
@@ -108,7 +106,7 @@ def _stream(s):
 
 
 def _call(name, *args):
-    rc = getattr(load(), name)(*args)
+    rc = getattr(_lib or load(), name)(*args)
     if rc != DG_OK:
         raise DgError(name, rc)
 

@@ -251,8 +251,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, stats=False, out=
         y = out if out is not None else torch.empty_like(x)
         mean = rstd = None
         if stats:
-            rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-            mean = None if rms else torch.empty(T, dtype=torch.float32, device=x.device)
+            rstd = x.new_empty(T, dtype=torch.float32)
+            mean = None if rms else x.new_empty(T, dtype=torch.float32)
         if T:
             _lib.dg_layer_norm(x, weight, bias, y, None, None, mean, rstd, T, K, eps, int(rms), _TYPES[x.dtype], w_type)
     return (y, mean, rstd) if stats else y
@@ -265,8 +265,8 @@ def layer_norm_cast(x, weight=None, bias=None, eps=1e-5, rms=False, stream=None)
     if K % 128:
         raise ValueError(f"K = {K} is not a multiple of 128")
     with _on(x.get_device(), stream):
-        q = torch.empty((T, K), dtype=torch.uint8, device=x.device)
-        sfa = (torch.zeros if T % 4 else torch.empty)((K // 128, _pad4(T)), dtype=torch.float32, device=x.device)
+        q = x.new_empty((T, K), dtype=torch.uint8)
+        sfa = (x.new_zeros if T % 4 else x.new_empty)((K // 128, _pad4(T)), dtype=torch.float32)
         if T:
             _lib.dg_layer_norm(x, weight, bias, None, q, sfa, None, None, T, K, eps, int(rms), _TYPES[x.dtype], w_type)
     return q, sfa
@@ -286,15 +286,15 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, rms=False, stream=
         raise ValueError("the RMS form has no bias")
     with _on(x.get_device(), stream):
         dx = torch.empty_like(x)
-        dw = torch.empty(K, dtype=torch.float32, device=x.device) if weight is not None else None
-        db = torch.empty(K, dtype=torch.float32, device=x.device) if bias else None
+        dw = x.new_empty(K, dtype=torch.float32) if weight is not None else None
+        db = x.new_empty(K, dtype=torch.float32) if bias else None
         if T == 0:
             for g in (dw, db):
                 if g is not None:
                     g.zero_()
             return dx, dw, db
         need = _lib.dg_layer_norm_backward_workspace(T, K) if weight is not None or bias else 0
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        ws = x.new_empty(need, dtype=torch.uint8) if need else None
         _lib.dg_layer_norm_backward(dy, x, weight, mean, rstd, dx, dw, db, ws, need, T, K, _TYPES[x.dtype], w_type)
     return dx, dw, db
 
@@ -315,8 +315,8 @@ def moe_route(logits, k, bias=None, groups=1, topk_groups=1, group_top=1, score=
         _check("bias", bias, (E,), torch.float32, logits.get_device())
     s = _score(score)
     with _on(logits.get_device(), stream):
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        ids = logits.new_empty((T, k), dtype=torch.int32)
+        weights = logits.new_empty((T, k), dtype=torch.float32)
         if T:
             _lib.dg_moe_route(logits, bias, ids, weights, T, E, k, groups, topk_groups, group_top, s, int(renorm), scale,
                               _TYPES[logits.dtype])
@@ -377,7 +377,7 @@ def cast_per_token_scatter_topk(x, dst_rows, M, G=1, out=None, stream=None):
         _check("out[1]", out[1], (G, K // 128, _pad4(M)), torch.float32, x.get_device())
     with _on(x.get_device(), stream):
         q, sfa = out if out is not None else (
-            torch.zeros((G * M, K), dtype=torch.uint8, device=x.device),
+            x.new_zeros((G * M, K), dtype=torch.uint8),
             torch.zeros((G, K // 128, _pad4(M)), dtype=torch.float32, device=x.device))
         if T and k and G * M:
             _lib.dg_cast_fp8_per_token_scatter_topk(x, dst_rows, q, sfa, T, k, G, M, K)
@@ -419,7 +419,7 @@ def moe_combine_backward(grad_y, d, dst_rows, weights=None, grouped_layout=None,
         _check("grouped_layout", grouped_layout, (R,), torch.int32, d.get_device())
     with _on(d.get_device(), stream):
         gd = (torch.zeros_like if grouped_layout is None else torch.empty_like)(d)
-        gw = torch.empty((T, k), dtype=torch.float32, device=d.device)
+        gw = d.new_empty((T, k), dtype=torch.float32)
         if T or (R and grouped_layout is not None):
             _lib.dg_moe_combine_backward(grad_y, d, dst_rows, weights, grouped_layout, gd, gw, T, k, N, R)
     return gd, gw
