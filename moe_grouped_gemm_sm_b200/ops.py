@@ -213,7 +213,15 @@ def _check_2d(name, t, dtype, device=None):
     _check(name, t, None, dtype, device)
     if t.dim() != 2:
         raise ValueError(f"{name}: two dimensions are wanted, got shape {tuple(t.shape)}")
+    _check_sizes(*t.shape)
     return t.shape
+
+
+def _check_sizes(*sizes):
+    """The C ABI takes 32-bit sizes; ctypes would cut larger ones off without a word."""
+    for s in sizes:
+        if not -2 ** 31 <= s < 2 ** 31:
+            raise ValueError(f"size {s} does not fit 32 bits")
 
 
 def _on(device, stream):
@@ -314,6 +322,7 @@ def moe_route(logits, k, bias=None, groups=1, topk_groups=1, group_top=1, score=
     if bias is not None:
         _check("bias", bias, (E,), torch.float32, logits.get_device())
     s = _score(score)
+    _check_sizes(k, groups, topk_groups, group_top)
     with _on(logits.get_device(), stream):
         ids = logits.new_empty((T, k), dtype=torch.int32)
         weights = logits.new_empty((T, k), dtype=torch.float32)
@@ -344,6 +353,7 @@ def moe_layout_contiguous(ids, G, M_sum=None, stream=None):
     T, k = _check_2d("ids", ids, torch.int32)
     if M_sum is None:
         M_sum = (T * k + 127 * min(G, T * k) + 127) // 128 * 128
+    _check_sizes(G, M_sum)
     with _on(ids.get_device(), stream):
         dst = torch.empty_like(ids)
         layout = ids.new_empty(M_sum)
@@ -356,6 +366,7 @@ def moe_layout_masked(ids, G, M_max, stream=None):
     """Rows of the masked layout for expert ids int32 [T,k] (ids outside [0,G) are dropped):
     (dst_rows int32 [T,k] with row g·M_max + i for expert g's i-th token, masked_m int32 [G])."""
     T, k = _check_2d("ids", ids, torch.int32)
+    _check_sizes(G, M_max)
     with _on(ids.get_device(), stream):
         dst = torch.empty_like(ids)
         masked_m = ids.new_empty(G)
@@ -372,6 +383,7 @@ def cast_per_token_scatter_topk(x, dst_rows, M, G=1, out=None, stream=None):
     _check("dst_rows", dst_rows, (T, k))
     if K % 128:
         raise ValueError(f"K = {K} is not a multiple of 128")
+    _check_sizes(M, G, G * M)
     if out is not None:
         _check("out[0]", out[0], (G * M, K), torch.uint8, x.get_device())
         _check("out[1]", out[1], (G, K // 128, _pad4(M)), torch.float32, x.get_device())
@@ -384,13 +396,22 @@ def cast_per_token_scatter_topk(x, dst_rows, M, G=1, out=None, stream=None):
     return q, sfa
 
 
+def _combine_sizes(d, dst_rows):
+    _check("d", d, None, torch.bfloat16)
+    if d.dim() < 2:
+        raise ValueError(f"d: two dimensions or more are wanted, got shape {tuple(d.shape)}")
+    T, k = _check_2d("dst_rows", dst_rows, torch.int32, d.get_device())
+    N = d.shape[-1]
+    R = d.numel() // max(N, 1)
+    _check_sizes(N, R)
+    return T, k, N, R
+
+
 def moe_combine(d, dst_rows, weights=None, c=None, out=None, stream=None):
     """y[t] = c[t] + sum_j weights[t,j]·d[dst_rows[t,j]] (bf16 [T,N]; d bf16 with rows of N, of any leading
     shape; negative rows are left out). ``out`` may be c. Without weights (ones) this is also the
     gradient of the dispatch."""
-    _check("d", d, None, torch.bfloat16)
-    T, k = _check_2d("dst_rows", dst_rows, torch.int32, d.get_device())
-    N = d.shape[-1]
+    T, k, N, R = _combine_sizes(d, dst_rows)
     if weights is not None:
         _check("weights", weights, (T, k), torch.float32, d.get_device())
     if c is not None:
@@ -400,7 +421,7 @@ def moe_combine(d, dst_rows, weights=None, c=None, out=None, stream=None):
     with _on(d.get_device(), stream):
         y = out if out is not None else d.new_empty((T, N))
         if T:
-            _lib.dg_moe_combine(d, dst_rows, weights, c, y, T, k, N, d.numel() // max(N, 1))
+            _lib.dg_moe_combine(d, dst_rows, weights, c, y, T, k, N, R)
     return y
 
 
@@ -408,10 +429,7 @@ def moe_combine_backward(grad_y, d, dst_rows, weights=None, grouped_layout=None,
     """Gradients (grad_d like d, grad_weights fp32 [T,k]) of moe_combine. Rows of grad_d that no pair
     maps to: with grouped_layout (int32 [M_sum]) its negative rows are zero and every other row has a
     pair; without it all of them are zero."""
-    _check("d", d, None, torch.bfloat16)
-    T, k = _check_2d("dst_rows", dst_rows, torch.int32, d.get_device())
-    N = d.shape[-1]
-    R = d.numel() // max(N, 1)
+    T, k, N, R = _combine_sizes(d, dst_rows)
     _check("grad_y", grad_y, (T, N), torch.bfloat16, d.get_device())
     if weights is not None:
         _check("weights", weights, (T, k), torch.float32, d.get_device())

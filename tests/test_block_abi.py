@@ -125,3 +125,11 @@ def test_host_tensors_are_refused():
                  lambda: ops.moe_combine(x, i), lambda: ops.moe_combine_backward(x, x, i)):
         with pytest.raises(ValueError, match="CUDA device"):
             call()
+
+
+def test_sizes_that_do_not_fit_the_abi_are_refused():
+    with pytest.raises(ValueError, match="32 bits"):
+        ops._check_sizes(5, 2 ** 31)
+    with pytest.raises(ValueError, match="32 bits"):
+        ops._check_sizes(-2 ** 31 - 1)
+    ops._check_sizes(0, -1, 2 ** 31 - 1)

@@ -72,6 +72,11 @@ def test_forward_in_place_and_no_rows():
     ref = ops.layer_norm(cuda(x), cuda(w), cuda(b))
     xd = cuda(x)
     assert ops.layer_norm(xd, cuda(w), cuda(b), out=xd) is xd and torch.equal(xd, ref)
+    for T, K, rms in ((400, 1024, False), (401, 777, False), (350, 128, True), (300, 8200, True)):   # many rows
+        x, w, b = make(T, K, torch.bfloat16, torch.float32, rms, seed=8)
+        ref = ops.layer_norm(cuda(x), cuda(w), cuda(b), rms=rms)
+        xd = cuda(x)
+        assert ops.layer_norm(xd, cuda(w), cuda(b), rms=rms, out=xd) is xd and torch.equal(xd, ref)
     e = torch.empty(0, 64, device="cuda")
     assert ops.layer_norm(e).shape == (0, 64)
     dx, dw, db = ops.layer_norm_backward(e, e, torch.ones(64, device="cuda"), e[:, 0], e[:, 0])
@@ -92,7 +97,8 @@ def test_constant_rows_and_large_offsets():
     assert ((y - ref).abs() <= tol + U).all()
 
 
-@pytest.mark.parametrize("T,K", [(1, 128), (5, 256), (6, 1024), (16, 7168), (301, 7168), (1000, 128), (3, 20480), (303, 1152)])
+@pytest.mark.parametrize("T,K", [(1, 128), (5, 256), (6, 1024), (16, 7168), (301, 7168), (1000, 128), (3, 20480), (303, 1152), (401, 256),
+                                 (310, 512), (300, 640), (300, 16384), (297, 8320)])
 @pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rms", [False, True])
 def test_cast(T, K, xt, rms):
@@ -114,6 +120,35 @@ def test_cast(T, K, xt, rms):
         sc = y.abs().amax(2) / 448
         assert torch.equal(sc, sfa.cpu()[:, :T].t())
         assert torch.equal((y / sc.unsqueeze(2)).view(T, K).to(torch.float8_e4m3fn).view(torch.uint8), q.cpu())
+
+
+@pytest.mark.parametrize("T,K", [(7, 384), (333, 384), (333, 2048)])
+def test_result_and_cast_in_one_call(T, K):
+    x, w, b = make(T, K, torch.bfloat16, torch.bfloat16, False, seed=9)
+    x, w, b = cuda(x), cuda(w), cuda(b)
+    y, mean, rstd = ops.layer_norm(x, w, b, stats=True)
+    q, sfa = ops.layer_norm_cast(x, w, b)
+    y2, q2, sfa2 = torch.empty_like(y), torch.empty_like(q), torch.zeros_like(sfa)
+    _lib.dg_layer_norm(x, w, b, y2, q2, sfa2, None, None, T, K, 1e-5, 0, 0, 0)
+    assert torch.equal(y, y2) and torch.equal(q, q2) and torch.equal(sfa, sfa2)
+
+
+@pytest.mark.parametrize("T,K", [(6, 520), (320, 520), (320, 1024), (320, 333), (320, 96)])
+@pytest.mark.parametrize("rms", [False, True])
+def test_bad_rows_stay_alone(T, K, rms):
+    """NaN, infinity and the lowest value in some rows leave every other row's bits as they were."""
+    x, w, b = make(T, K, torch.float32, torch.float32, rms, seed=10)
+    dy = torch.randn(T, K, generator=torch.Generator().manual_seed(3))
+    bad = torch.zeros(T, dtype=torch.bool)
+    bad[[1, 2, T - 1]] = True
+    xb = x.clone()
+    xb[1, 3], xb[2, K - 1], xb[T - 1, 0] = float("nan"), float("inf"), -3.4e38
+    outs = []
+    for v in (x, xb):
+        y, mean, rstd = ops.layer_norm(cuda(v), cuda(w), cuda(b), rms=rms, stats=True)
+        dx = ops.layer_norm_backward(cuda(dy), cuda(v), cuda(w), mean, rstd, bias=not rms, rms=rms)[0]
+        outs.append([t.cpu()[~bad] for t in (y, rstd, dx)])
+    assert all(torch.equal(p, q) for p, q in zip(*outs))
 
 
 def test_cast_of_zero_rows():
