@@ -81,11 +81,14 @@ NormRingShape norm_ring_shape(int T, int K, int x_type, int tensors) {
     s.teams = s.threads == 32 ? 4 : 1;
     if (s.cols && K == s.n * s.threads) s.cols = dg::COLS_EXACT;
     const size_t row = static_cast<size_t>(dg::NORM_STAGES) * tensors * (s.cols ? K : (K + 2 * c - 2) / c * c) * size;
-    s.r = s.n <= 16 && 2 * row <= static_cast<size_t>(kNormRing) ? 2 : 1;
+    // two rows a step where the rings of the blocks that the threads allow still fit an SM: 8192 x 4096 fp32
+    // backward takes 86 us with one block of two rows an SM
+    const int most = std::max(1, dg::NORM_RING_THREADS / (s.threads * s.teams));
+    s.r = s.n <= 16 && 2 * row * s.teams * most <= static_cast<size_t>(220 << 10) && 2 * row <= static_cast<size_t>(kNormRing) ? 2 : 1;
     if (s.threads > dg::NORM_RING_THREADS || (s.n == 32 && !s.cols) || s.r * row > static_cast<size_t>(kNormRing)) return s;
     s.smem = s.teams * s.r * row;
-    const int per_sm = std::min(dg::NORM_RING_THREADS / (s.threads * s.teams), static_cast<int>((220 << 10) / s.smem));
-    s.blocks = std::min((T + s.teams - 1) / s.teams, kNormSms * std::max(1, per_sm));
+    const int per_sm = std::max(1, std::min(most, static_cast<int>((220 << 10) / s.smem)));
+    s.blocks = std::min((T + s.teams - 1) / s.teams, kNormSms * per_sm);
     return s;
 }
 
