@@ -256,7 +256,10 @@ __device__ __forceinline__ void sort_falling(float (&v)[N]) {
 // chosen wrongly: then all that may belong to the k largest, one in a lane, are put in the order of
 // their 64-bit values, and groups at the border likewise. Neighbours with the same logit and the
 // same bias are equal in truth and need no second look. With N(0,1.5) logits over 256 experts that
-// is about one token in 300.
+// is about 40 of 16384 tokens.
+// Bound by instructions (1030 a token and warp with 8 groups over 256 experts, 63 % of the issue slots used): 16384 tokens
+// take 23.5 us, 65536 80 us; every value in 64 bits took 122 us. Traffic alone would be 2.7 us for 16384. 8 blocks an SM
+// (64 registers, some spilled) are faster than 6 or 4 without spills: 80 against 96 us for 65536 tokens.
 template <typename LT, int EPL>
 __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&b)[EPL], int t, int lane) {
     const bool softmax = p.score == SCORE_SOFTMAX, by_logit = p.bias == nullptr;

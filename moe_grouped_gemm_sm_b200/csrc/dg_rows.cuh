@@ -16,7 +16,8 @@ namespace dg {
 // One cluster of up to 16 blocks does it in one launch and without scratch in global memory: each block
 // counts its consecutive pairs per warp and expert, the blocks read each other's counts through distributed
 // shared memory, and each places its own pairs. Latency-bound throughout (131072 pairs over 256 experts are
-// 0.3 us of traffic); two launches over 64 blocks with the counts in global memory took 14-17 us.
+// 0.3 us of traffic, and take 10.8 us; 1024 pairs 3.0); two launches over 64 blocks with the counts in global
+// memory took 14 to 17 us, and needed scratch.
 // Equal ids of a warp are found by one ballot per bit of the id (BITS, unrolled); the match instruction took some
 // 400 cycles.
 // -----------------------------------------------------------------------------------------------
