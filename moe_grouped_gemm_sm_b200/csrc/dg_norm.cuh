@@ -682,16 +682,17 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(
     }
     // mean and rstd of the team's next 32 rows, one a lane: a load for each step's rows, prefetched a step ahead, was
     // waited for together with reads of the ring (85 us instead of 69 for 8192 x 7168, by the compiler's choice)
-    float mean32 = 0.f, rstd32 = 0.f;
+    float mean32, rstd32;
+    const auto statistics = [&](int first) {
+        const int at = first + lane * step;
+        rstd32 = at < p.T ? p.rstd[at] : 0.f;
+        mean32 = at < p.T && p.mean ? p.mean[at] : 0.f;
+    };
+    statistics(row);
     int stage = 0;
     for (int n = 0; row < p.T; ++n, row += R * step) {
         ring_step<VEC>([&] { fetch(row + (NORM_STAGES - 1) * R * step, stage == 0 ? NORM_STAGES - 1 : stage - 1); });
-        if (n * R % 32 == 0) {
-            const int at = row + lane * step;
-            const bool in = at < p.T;
-            rstd32 = in ? p.rstd[at] : 0.f;
-            mean32 = in && p.mean ? p.mean[at] : 0.f;
-        }
+        if (n > 0 && n * R % 32 == 0) statistics(row);
         float mu[R], r[R];
 #pragma unroll
         for (int q = 0; q < R; ++q) {

@@ -16,6 +16,7 @@ explicit functions; no autograd graph is built.
 from __future__ import annotations
 
 import contextlib
+import functools
 
 import torch
 
@@ -193,6 +194,11 @@ _SCORES = {"softmax": 0, "sigmoid": 1}               # dg_score
 _HERE = contextlib.nullcontext()
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(T, K):
+    return _lib.dg_layer_norm_backward_workspace(T, K)
+
+
 def _check(name, t, shape=None, dtype=None, device=None):
     """A contiguous CUDA tensor of this shape and dtype (or one of these dtypes) on this device (index)."""
     if not isinstance(t, torch.Tensor):
@@ -301,7 +307,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, rms=False, stream=
                 if g is not None:
                     g.zero_()
             return dx, dw, db
-        need = _lib.dg_layer_norm_backward_workspace(T, K) if weight is not None or bias else 0
+        need = _norm_workspace(T, K) if weight is not None or bias else 0
         ws = x.new_empty(need, dtype=torch.uint8) if need else None
         _lib.dg_layer_norm_backward(dy, x, weight, mean, rstd, dx, dw, db, ws, need, T, K, _TYPES[x.dtype], w_type)
     return dx, dw, db
