@@ -267,3 +267,23 @@ def test_refusals():
     with pytest.raises(_lib.DgError) as e:
         ops.layer_norm(torch.zeros(4 * 64 + 8, dtype=torch.bfloat16, device="cuda")[4:260].view(4, 64))
     assert e.value.status == _lib.DG_ERR_ALIGNMENT
+
+
+def test_more_than_2_to_31_elements():
+    """Offsets that pass 32 bits: 270000 rows of 8192, the last ones compared with the same rows alone."""
+    T, K = 270000, 8192
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    last, w, b = make(5, K, torch.bfloat16, torch.float32, False, seed=11)
+    x[-5:] = cuda(last)
+    y, mean, rstd = ops.layer_norm(x, cuda(w), cuda(b), stats=True)
+    ref, mu, r, tol = ref_forward(last, w, b, 1e-5, False)
+    assert ((y[-5:].cpu().double() - ref).abs() <= tol + 2.0 ** -8 * (ref.abs() + tol)).all()
+    assert torch.equal(y[0], cuda(b).bfloat16()) and torch.equal(y[T // 2], y[0])
+    dy = torch.zeros_like(x)
+    dl = torch.randn(5, K, generator=torch.Generator().manual_seed(4)).bfloat16()
+    dy[-5:] = cuda(dl)
+    dx, dw, db = ops.layer_norm_backward(dy, x, cuda(w), mean, rstd)
+    rx, tx, rw, tw, rb, tb = ref_backward(dl, last, w, mean[-5:].cpu(), rstd[-5:].cpu(), False)
+    assert ((dx[-5:].cpu().double() - rx).abs() <= tx + 2.0 ** -8 * (rx.abs() + tx)).all()
+    assert not dx[:T - 5].any()
+    assert ((dw.cpu().double() - rw).abs() <= tw).all() and ((db.cpu().double() - rb).abs() <= tb).all()
