@@ -16,55 +16,37 @@ constexpr int kMaxRows = 1 << 30;
 
 bool valid_type(int t) { return t == DG_BF16 || t == DG_FP32; }
 
-// Threads and vectors per thread of a norm kernel: one warp a row, 8 rows a block, for rows of up to
-// 4 vectors a lane; else a block a row. Few rows (fewer than two blocks per SM) spread a row
-// over as many threads as it has vectors; many rows keep 4 vectors in flight per thread.
-struct NormShape {
-    int vpt;
-    dim3 grid, block;
-};
-
-NormShape norm_shape(int T, int nv, int sm_count, int max_threads) {
-    NormShape s;
-    if (nv <= 128) {
-        s.vpt = nv <= 32 ? 1 : (nv <= 64 ? 2 : 4);
-        s.block = dim3(32, 8, 1);
-        s.grid = dim3(static_cast<unsigned>((T + 7) / 8), 1, 1);
-        return s;
-    }
-    s.vpt = T < 2 * sm_count ? 1 : 4;
-    while ((nv + s.vpt - 1) / s.vpt > max_threads) s.vpt *= 2;
-    const int nt = ((nv + s.vpt - 1) / s.vpt + 31) / 32 * 32;
-    s.block = dim3(static_cast<unsigned>(nt), 1, 1);
-    s.grid = dim3(static_cast<unsigned>(T), 1, 1);
-    return s;
-}
-
-// f(vector size, vectors per thread, shape) with the first two as compile-time constants. Rows
-// that are not whole 16-byte vectors go element by element (V = 1). MAXT threads and the K limit
-// bound the vectors per thread at kNormMaxK / (V·MAXT).
-template <typename XT, int MAXT, typename F>
+// f(vector size, vectors per thread, grid, block) of the register kernel, the first two as compile-time constants: one
+// warp a row, 8 rows a block, for rows of up to 4 vectors a lane; else a block a row. Few rows (fewer than two
+// blocks per SM) spread a row over as many threads as it has vectors; many rows keep 4 vectors in flight per
+// thread. Rows that are not whole 16-byte vectors go element by element (V = 1, 4 or 32 a thread).
+template <typename XT, typename F>
 dg_status norm_dispatch(int T, int K, int sm_count, F f) {
-    constexpr int V = 16 / static_cast<int>(sizeof(XT)), TOP = kNormMaxK / (V * MAXT);
+    constexpr int VMAX = 16 / static_cast<int>(sizeof(XT));
     using std::integral_constant;
-    if (K % V == 0) {
-        const NormShape s = norm_shape(T, K / V, sm_count, MAXT);
-        if (s.vpt == 1) return f(integral_constant<int, V>(), integral_constant<int, 1>(), s);
-        if (s.vpt == 2) return f(integral_constant<int, V>(), integral_constant<int, 2>(), s);
-        if (s.vpt == 4) return f(integral_constant<int, V>(), integral_constant<int, 4>(), s);
-        if constexpr (TOP >= 8)
-            if (s.vpt == 8) return f(integral_constant<int, V>(), integral_constant<int, 8>(), s);
-        if constexpr (TOP >= 16)
-            if (s.vpt == 16) return f(integral_constant<int, V>(), integral_constant<int, 16>(), s);
-        return DG_ERR_INVALID_ARG;
+    const int v = K % VMAX == 0 ? VMAX : 1, nv = K / v;
+    int vpt = T < 2 * sm_count ? 1 : 4;
+    dim3 block(32, 8, 1), grid(static_cast<unsigned>((T + 7) / 8), 1, 1);
+    if (nv <= 128) {
+        vpt = nv <= 32 ? 1 : (nv <= 64 ? 2 : 4);
+    } else {
+        while ((nv + vpt - 1) / vpt > dg::NORM_MAX_THREADS) vpt *= 2;
+        block = dim3(static_cast<unsigned>(((nv + vpt - 1) / vpt + 31) / 32 * 32), 1, 1);
+        grid = dim3(static_cast<unsigned>(T), 1, 1);
     }
-    const NormShape s = norm_shape(T, K, sm_count, MAXT);
-    if (s.vpt <= 4) return f(integral_constant<int, 1>(), integral_constant<int, 4>(), s);
-    return f(integral_constant<int, 1>(), integral_constant<int, TOP * V>(), s);
+    if (v == 1) {
+        if (vpt <= 4) return f(integral_constant<int, 1>(), integral_constant<int, 4>(), grid, block);
+        return f(integral_constant<int, 1>(), integral_constant<int, 32>(), grid, block);
+    }
+    if (vpt == 1) return f(integral_constant<int, VMAX>(), integral_constant<int, 1>(), grid, block);
+    if (vpt == 2) return f(integral_constant<int, VMAX>(), integral_constant<int, 2>(), grid, block);
+    if constexpr (VMAX == 4)   // fp32 rows of more than 16384
+        if (vpt == 8) return f(integral_constant<int, VMAX>(), integral_constant<int, 8>(), grid, block);
+    return f(integral_constant<int, VMAX>(), integral_constant<int, 4>(), grid, block);
 }
 
-// Launch shape of the ring kernels (`tensors` rows side by side: 1 forward, 2 backward): 16 columns a
-// thread, 8 for rows of up to 256, 32 for rows of more than 8192, 16 single ones where rows are not whole vectors; two rows per
+// Launch shape of the ring kernels (`tensors` rows side by side: 1 forward, 2 backward): 16 columns a thread, 8 for
+// rows of up to 256, 32 for rows of more than 8192, 16 single ones where rows are not whole vectors; two rows per
 // step where the ring holds them. Warps as teams for rows of one warp; otherwise a block a row, and as many
 // blocks per SM as 512 threads and the rings allow. blocks = 0: the row is too long.
 struct NormRingShape {
@@ -84,10 +66,11 @@ NormRingShape norm_ring_shape(int T, int K, int x_type, int tensors) {
     // two rows a step where the rings of the blocks that the threads allow still fit an SM: 8192 x 4096 fp32
     // backward takes 86 us with one block of two rows an SM
     const int most = std::max(1, dg::NORM_RING_THREADS / (s.threads * s.teams));
-    s.r = s.n <= 16 && 2 * row * s.teams * most <= static_cast<size_t>(220 << 10) && 2 * row <= static_cast<size_t>(kNormRing) ? 2 : 1;
-    if (s.threads > dg::NORM_RING_THREADS || (s.n == 32 && !s.cols) || s.r * row > static_cast<size_t>(kNormRing)) return s;
+    const size_t ring = static_cast<size_t>(kNormRing), sm = static_cast<size_t>(220 << 10);
+    s.r = s.n <= 16 && 2 * row * s.teams * most <= sm && 2 * row <= ring ? 2 : 1;
+    if (s.threads > dg::NORM_RING_THREADS || (s.n == 32 && !s.cols) || s.r * row > ring) return s;
     s.smem = s.teams * s.r * row;
-    const int per_sm = std::max(1, std::min(most, static_cast<int>((220 << 10) / s.smem)));
+    const int per_sm = std::max(1, std::min(most, static_cast<int>(sm / s.smem)));
     s.blocks = std::min((T + s.teams - 1) / s.teams, kNormSms * per_sm);
     // Backward: two rows a block at least, once every SM has a block; its part of dw and db is as long as a row
     // (1000 x 1024 bf16 10.0 us, one row a block 11.4; 2000 x 1001 fp32 15.8 and 18.3; four rows 8.3 and 20.8).
@@ -138,8 +121,8 @@ dg_status run_layer_norm(const dg::NormParams &p, int x_type, int sm_count, cuda
                                                     : launch_layer_norm_ring<XT, WT, 16, 2, dg::COLS_SINGLE>(p, s, st);
         }
     }
-    return norm_dispatch<XT, dg::NORM_MAX_THREADS>(p.T, p.K, sm_count, [&](auto v, auto vpt, const NormShape &s) {
-        Launch ln(s.grid, s.block, 0, st);
+    return norm_dispatch<XT>(p.T, p.K, sm_count, [&](auto v, auto vpt, dim3 grid, dim3 block) {
+        Launch ln(grid, block, 0, st);
         return from_cuda(cudaLaunchKernelEx(
             &ln.cfg, dg::layer_norm_kernel<XT, WT, decltype(v)::value, decltype(vpt)::value>, p));
     });
@@ -156,8 +139,20 @@ dg_status launch_norm_backward(const dg::NormBackParams &p, const NormRingShape 
     return launch_norm_ring<dg::NormBackParams>(dg::layer_norm_backward_kernel<XT, WT, N, R, COLS>, ready, p, s, st);
 }
 
+// Rows too long for the ring (bf16 above 16384, fp32 above 8533, single columns above 8192): dx by a block a row,
+// 8 or 16 vectors or 64 elements a thread, then the column sums.
+template <typename XT, typename WT, int V, int VPT>
+dg_status launch_norm_long(const dg::NormBackParams &p, cudaStream_t st) {
+    const int nt = ((p.K / V + VPT - 1) / VPT + 31) / 32 * 32;
+    Launch ln(dim3(static_cast<unsigned>(p.T), 1, 1), dim3(static_cast<unsigned>(nt), 1, 1), 0, st);
+    const dg_status s = from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::layer_norm_dx_kernel<XT, WT, V, VPT>, p));
+    if (s != DG_OK || !p.part) return s;
+    Launch sums(dim3(static_cast<unsigned>((p.K + 31) / 32), static_cast<unsigned>(p.parts), 1), dim3(32, 8, 1), 0, st);
+    return from_cuda(cudaLaunchKernelEx(&sums.cfg, dg::layer_norm_dwdb_kernel<XT>, p));
+}
+
 template <typename XT, typename WT>
-dg_status run_layer_norm_backward(dg::NormBackParams p, int x_type, int sm_count, cudaStream_t st) {
+dg_status run_layer_norm_backward(dg::NormBackParams p, int x_type, cudaStream_t st) {
     const NormRingShape sh = norm_ring_shape(p.T, p.K, x_type, 2);
     p.parts = norm_parts(p.T, p.K, x_type);
     if (!p.dw && !p.db) p.part = nullptr;
@@ -179,26 +174,25 @@ dg_status run_layer_norm_backward(dg::NormBackParams p, int x_type, int sm_count
             s = sh.r == 2 ? launch_norm_backward<XT, WT, 16, 2, dg::COLS_SINGLE>(p, sh, st)
                           : launch_norm_backward<XT, WT, 16, 1, dg::COLS_SINGLE>(p, sh, st);
     } else {
-        s = norm_dispatch<XT, dg::NORM_DX_MAX_THREADS>(p.T, p.K, sm_count, [&](auto v, auto vpt, const NormShape &shape) {
-            Launch ln(shape.grid, shape.block, 0, st);
-            return from_cuda(cudaLaunchKernelEx(
-                &ln.cfg, dg::layer_norm_dx_kernel<XT, WT, decltype(v)::value, decltype(vpt)::value>, p));
-        });
-        if (s == DG_OK && p.part) {
-            Launch ln(dim3(static_cast<unsigned>((p.K + 31) / 32), static_cast<unsigned>(p.parts), 1), dim3(32, 8, 1), 0, st);
-            s = from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::layer_norm_dwdb_kernel<XT>, p));
-        }
+        constexpr int V = 16 / static_cast<int>(sizeof(XT));
+        if (p.K % V != 0)
+            s = launch_norm_long<XT, WT, 1, 64>(p, st);
+        else if (p.K <= V * 8 * dg::NORM_DX_MAX_THREADS)
+            s = launch_norm_long<XT, WT, V, 8>(p, st);
+        else if constexpr (V == 4)
+            s = launch_norm_long<XT, WT, V, 16>(p, st);
+        else
+            s = DG_ERR_INVALID_ARG;   // no bf16 row is longer than 8·8·512
     }
     if (s != DG_OK || !p.part) return s;
     Launch ln(dim3(static_cast<unsigned>((p.K + 31) / 32), 2, 1), dim3(32, 16, 1), 0, st);
     return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::layer_norm_parts_kernel, p));
 }
 
-
 // Argument checks that both directions of the routing share.
 dg_status check_route(int T, int E, int k, int score, int dtype) {
-    if (T < 0 || T > kMaxRows || E <= 0 || E > dg::ROUTE_MAX_E || k <= 0 || k > dg::ROUTE_MAX_K || k > E || !valid_type(dtype) ||
-        (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID))
+    if (T < 0 || T > kMaxRows || E <= 0 || E > dg::ROUTE_MAX_E || k <= 0 || k > dg::ROUTE_MAX_K || k > E ||
+        !valid_type(dtype) || (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID))
         return DG_ERR_INVALID_ARG;
     return DG_OK;
 }
@@ -276,7 +270,8 @@ extern "C" {
 
 dg_status dg_layer_norm(const void *x, const void *weight, const void *bias, void *y, void *q, float *sfa, float *mean,
                         float *rstd, int T, int K, float eps, int rms, int x_type, int w_type, void *stream) {
-    if (!x || (!y && !q) || (q != nullptr) != (sfa != nullptr) || T < 0 || T > kMaxRows || K <= 0 || K > kNormMaxK || !(eps >= 0.f) ||
+    if (!x || (!y && !q) || (q != nullptr) != (sfa != nullptr) || T < 0 || T > kMaxRows || K <= 0 || K > kNormMaxK ||
+        !(eps >= 0.f) ||
         !valid_type(x_type) || !valid_type(w_type) || (rms && bias) || (q && K % 128 != 0))
         return DG_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(weight) || !aligned16(bias) || !aligned16(y) || !aligned16(q) || !aligned16(sfa))
@@ -315,7 +310,8 @@ long long dg_layer_norm_backward_workspace(int T, int K) {
 dg_status dg_layer_norm_backward(const void *dy, const void *x, const void *weight, const float *mean, const float *rstd,
                                  void *dx, float *dw, float *db, void *workspace, long long workspace_bytes, int T, int K,
                                  int x_type, int w_type, void *stream) {
-    if (!dy || !x || !rstd || !dx || T < 0 || T > kMaxRows || K <= 0 || K > kNormMaxK || !valid_type(x_type) || !valid_type(w_type))
+    if (!dy || !x || !rstd || !dx || T < 0 || T > kMaxRows || K <= 0 || K > kNormMaxK || !valid_type(x_type) ||
+        !valid_type(w_type))
         return DG_ERR_INVALID_ARG;
     if ((dw || db) && T > 0 && (!workspace || workspace_bytes < dg_layer_norm_backward_workspace(T, K)))
         return DG_ERR_INVALID_ARG;
@@ -345,10 +341,10 @@ dg_status dg_layer_norm_backward(const void *dy, const void *x, const void *weig
     p.T = T;
     p.K = K;
     if (x_type == DG_BF16)
-        return w_type == DG_BF16 ? run_layer_norm_backward<__nv_bfloat16, __nv_bfloat16>(p, x_type, di->sm_count, st)
-                                 : run_layer_norm_backward<__nv_bfloat16, float>(p, x_type, di->sm_count, st);
-    return w_type == DG_BF16 ? run_layer_norm_backward<float, __nv_bfloat16>(p, x_type, di->sm_count, st)
-                             : run_layer_norm_backward<float, float>(p, x_type, di->sm_count, st);
+        return w_type == DG_BF16 ? run_layer_norm_backward<__nv_bfloat16, __nv_bfloat16>(p, x_type, st)
+                                 : run_layer_norm_backward<__nv_bfloat16, float>(p, x_type, st);
+    return w_type == DG_BF16 ? run_layer_norm_backward<float, __nv_bfloat16>(p, x_type, st)
+                             : run_layer_norm_backward<float, float>(p, x_type, st);
 }
 
 dg_status dg_moe_route(const void *logits, const float *bias, int32_t *ids, float *weights, int T, int E, int k,
@@ -458,7 +454,8 @@ dg_status dg_cast_fp8_per_token_scatter_topk(const void *x, const int32_t *dst_r
 
 dg_status dg_moe_combine(const void *d, const int32_t *dst_rows, const float *weights, const void *c, void *y, int T,
                          int k, int N, int R, void *stream) {
-    if ((R > 0 && !d) || (T > 0 && (!dst_rows || !y)) || T < 0 || T > kMaxRows || k <= 0 || k > dg::COMBINE_MAX_K || N <= 0 || N % 8 != 0 || R < 0)
+    if ((R > 0 && !d) || (T > 0 && (!dst_rows || !y)) || T < 0 || T > kMaxRows || k <= 0 ||
+        k > dg::COMBINE_MAX_K || N <= 0 || N % 8 != 0 || R < 0)
         return DG_ERR_INVALID_ARG;
     if (!aligned16(d) || !aligned16(c) || !aligned16(y)) return DG_ERR_ALIGNMENT;
     if (T == 0) return DG_OK;
@@ -486,7 +483,8 @@ dg_status dg_moe_combine_backward(const void *grad_y, const void *d, const int32
                                   const int32_t *grouped_layout, void *grad_d, float *grad_weights, int T, int k, int N,
                                   int R, void *stream) {
     if ((T > 0 && (!grad_y || !dst_rows)) || (T > 0 && R > 0 && !grad_d && !grad_weights) ||
-        (R > 0 && grad_weights && !d) || (grouped_layout && !grad_d) || T < 0 || T > kMaxRows || k <= 0 || k > dg::COMBINE_MAX_K || N <= 0 || N % 8 != 0 || R < 0)
+        (R > 0 && grad_weights && !d) || (grouped_layout && !grad_d) || T < 0 || T > kMaxRows || k <= 0 ||
+        k > dg::COMBINE_MAX_K || N <= 0 || N % 8 != 0 || R < 0)
         return DG_ERR_INVALID_ARG;
     if (!aligned16(grad_y) || !aligned16(d) || !aligned16(grad_d)) return DG_ERR_ALIGNMENT;
     const DeviceInfo *di = nullptr;

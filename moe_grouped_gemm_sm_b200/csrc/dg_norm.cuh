@@ -240,7 +240,8 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) layer_norm_kernel(const Norm
 #pragma unroll
                 for (int e = 0; e < V; ++e) f[j][e] += w[e];
             }
-            if (p.y) store_vec<XT, V>(static_cast<XT *>(p.y) + static_cast<size_t>(row) * K + static_cast<size_t>(i) * V, f[j]);
+            XT *y = static_cast<XT *>(p.y) + static_cast<size_t>(row) * K + static_cast<size_t>(i) * V;
+            if (p.y) store_vec<XT, V>(y, f[j]);
         }
         if constexpr (V > 1) {
             if (p.q) {   // K % 128 == 0: the threads of a slice are all inside the row or all outside
@@ -485,7 +486,8 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_ring_kernel(cons
             m2[0] = warp_sum(m2[0]);
         }
         if (nt > 32) {
-            if (lane < R) s_red[n & 1][lane][tid >> 5] = make_float2(R == 2 && lane ? mu[R - 1] : mu[0], R == 2 && lane ? m2[R - 1] : m2[0]);
+            const int q_of = R == 2 && lane ? 1 : 0;
+            if (lane < R) s_red[n & 1][lane][tid >> 5] = make_float2(q_of ? mu[R - 1] : mu[0], q_of ? m2[R - 1] : m2[0]);
             __syncthreads();   // the other half of s_red is free: all have left the last rows' sums
             const float c = static_cast<float>(count_of_lane);
             float2 v[R];

@@ -385,7 +385,8 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
             // their 64-bit values; the others are truly above or below all of those.
             const float in = -redux_max(keep ? -mine : -CUDART_INF_F);
             const float out = redux_max(keep ? -CUDART_INF_F : mine);
-            const float tol = 2.f * (by_logit ? (softmax ? 0x1p-17f : 0x1p-20f) : tol_score) + 0x1p-21f * (fabsf(in) + fabsf(out));
+            const float unit = by_logit ? (softmax ? 0x1p-17f : 0x1p-20f) : tol_score;
+            const float tol = 2.f * unit + 0x1p-21f * (fabsf(in) + fabsf(out));
             if (out > -CUDART_INF_F && !(in - out > tol)) {
                 const bool open = lane < p.groups && !(keep ? mine - out > tol : in - mine > tol);
                 const uint32_t compete = __ballot_sync(0xFFFFFFFFu, open);

@@ -15,7 +15,6 @@ explicit functions; no autograd graph is built.
 """
 from __future__ import annotations
 
-import contextlib
 import functools
 
 import torch
@@ -191,7 +190,6 @@ def k_grouped_fp8_gemm_tn_contiguous(a, sfa, b, sfb, ks, c=None, out=None, strea
 
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}       # dg_dtype
 _SCORES = {"softmax": 0, "sigmoid": 1}               # dg_score
-_HERE = contextlib.nullcontext()
 
 
 @functools.lru_cache(maxsize=1024)
@@ -217,29 +215,38 @@ def _check(name, t, shape=None, dtype=None, device=None):
 
 def _check_2d(name, t, dtype, device=None):
     _check(name, t, None, dtype, device)
-    if t.dim() != 2:
-        raise ValueError(f"{name}: two dimensions are wanted, got shape {tuple(t.shape)}")
-    _check_sizes(*t.shape)
-    return t.shape
+    s = t.shape
+    if len(s) != 2:
+        raise ValueError(f"{name}: two dimensions are wanted, got shape {tuple(s)}")
+    _check_sizes(*s)
+    return s
 
 
 def _check_sizes(*sizes):
     """The C ABI takes 32-bit sizes; ctypes would cut larger ones off without a word."""
-    for s in sizes:
-        if not -2 ** 31 <= s < 2 ** 31:
-            raise ValueError(f"size {s} does not fit 32 bits")
+    if max(sizes) >= 2 ** 31 or min(sizes) < -2 ** 31:
+        raise ValueError(f"sizes {sizes} do not fit 32 bits")
+
+
+def _elsewhere(device, stream):
+    """Whether a call has to change the current device or stream first (_on)."""
+    return stream is not None or device != torch._C._cuda_getDevice()
 
 
 def _on(device, stream):
     """Makes the device (an index) and ``stream`` current: kernels run there, and what is allocated inside
     belongs to that stream, so that a workspace is not handed out again while it is in use."""
     if stream is None:
-        return _HERE if device == torch.cuda.current_device() else torch.cuda.device(device)
+        return torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     if stream.device.index != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{device}")
     return torch.cuda.stream(stream)
+
+
+# The current stream of a device (index) as a raw handle; through a Stream object it takes 3 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _norm_args(x, weight, bias, rms):
@@ -261,14 +268,18 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, stats=False, out=
     T, K, w_type = _norm_args(x, weight, bias, rms)
     if out is not None:
         _check("out", out, (T, K), x.dtype, x.get_device())
-    with _on(x.get_device(), stream):
-        y = out if out is not None else torch.empty_like(x)
-        mean = rstd = None
-        if stats:
-            rstd = x.new_empty(T, dtype=torch.float32)
-            mean = None if rms else x.new_empty(T, dtype=torch.float32)
-        if T:
-            _lib.dg_layer_norm(x, weight, bias, y, None, None, mean, rstd, T, K, eps, int(rms), _TYPES[x.dtype], w_type)
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return layer_norm(x, weight, bias, eps, rms, stats, out)
+    y = out if out is not None else torch.empty_like(x)
+    mean = rstd = None
+    if stats:
+        rstd = x.new_empty(T, dtype=torch.float32)
+        mean = None if rms else x.new_empty(T, dtype=torch.float32)
+    if T:
+        _lib.dg_layer_norm(x, weight, bias, y, None, None, mean, rstd, T, K, eps, int(rms), _TYPES[x.dtype], w_type,
+                           _raw_stream(dev))
     return (y, mean, rstd) if stats else y
 
 
@@ -278,11 +289,15 @@ def layer_norm_cast(x, weight=None, bias=None, eps=1e-5, rms=False, stream=None)
     T, K, w_type = _norm_args(x, weight, bias, rms)
     if K % 128:
         raise ValueError(f"K = {K} is not a multiple of 128")
-    with _on(x.get_device(), stream):
-        q = x.new_empty((T, K), dtype=torch.uint8)
-        sfa = (x.new_zeros if T % 4 else x.new_empty)((K // 128, _pad4(T)), dtype=torch.float32)
-        if T:
-            _lib.dg_layer_norm(x, weight, bias, None, q, sfa, None, None, T, K, eps, int(rms), _TYPES[x.dtype], w_type)
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return layer_norm_cast(x, weight, bias, eps, rms)
+    q = x.new_empty((T, K), dtype=torch.uint8)
+    sfa = (x.new_zeros if T % 4 else x.new_empty)((K // 128, _pad4(T)), dtype=torch.float32)
+    if T:
+        _lib.dg_layer_norm(x, weight, bias, None, q, sfa, None, None, T, K, eps, int(rms), _TYPES[x.dtype], w_type,
+                           _raw_stream(dev))
     return q, sfa
 
 
@@ -298,18 +313,22 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, rms=False, stream=
         _check("mean", mean, (T,), torch.float32, x.get_device())
     if rms and bias:
         raise ValueError("the RMS form has no bias")
-    with _on(x.get_device(), stream):
-        dx = torch.empty_like(x)
-        dw = x.new_empty(K, dtype=torch.float32) if weight is not None else None
-        db = x.new_empty(K, dtype=torch.float32) if bias else None
-        if T == 0:
-            for g in (dw, db):
-                if g is not None:
-                    g.zero_()
-            return dx, dw, db
-        need = _norm_workspace(T, K) if weight is not None or bias else 0
-        ws = x.new_empty(need, dtype=torch.uint8) if need else None
-        _lib.dg_layer_norm_backward(dy, x, weight, mean, rstd, dx, dw, db, ws, need, T, K, _TYPES[x.dtype], w_type)
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return layer_norm_backward(dy, x, weight, mean, rstd, bias, rms)
+    dx = torch.empty_like(x)
+    dw = x.new_empty(K, dtype=torch.float32) if weight is not None else None
+    db = x.new_empty(K, dtype=torch.float32) if bias else None
+    if T == 0:
+        for g in (dw, db):
+            if g is not None:
+                g.zero_()
+        return dx, dw, db
+    need = _norm_workspace(T, K) if weight is not None or bias else 0
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
+    _lib.dg_layer_norm_backward(dy, x, weight, mean, rstd, dx, dw, db, ws, need, T, K, _TYPES[x.dtype], w_type,
+                                _raw_stream(dev))
     return dx, dw, db
 
 
@@ -329,12 +348,15 @@ def moe_route(logits, k, bias=None, groups=1, topk_groups=1, group_top=1, score=
         _check("bias", bias, (E,), torch.float32, logits.get_device())
     s = _score(score)
     _check_sizes(k, groups, topk_groups, group_top)
-    with _on(logits.get_device(), stream):
-        ids = logits.new_empty((T, k), dtype=torch.int32)
-        weights = logits.new_empty((T, k), dtype=torch.float32)
-        if T:
-            _lib.dg_moe_route(logits, bias, ids, weights, T, E, k, groups, topk_groups, group_top, s, int(renorm), scale,
-                              _TYPES[logits.dtype])
+    dev = logits.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_route(logits, k, bias, groups, topk_groups, group_top, score, renorm, scale)
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
+    if T:
+        _lib.dg_moe_route(logits, bias, ids, weights, T, E, k, groups, topk_groups, group_top, s, int(renorm), scale,
+                          _TYPES[logits.dtype], _raw_stream(dev))
     return weights, ids
 
 
@@ -345,10 +367,14 @@ def moe_route_backward(grad_weights, logits, ids, score="softmax", renorm=True, 
     _check("ids", ids, (T, k))
     _check("grad_weights", grad_weights, (T, k), torch.float32, logits.get_device())
     s = _score(score)
-    with _on(logits.get_device(), stream):
-        g = torch.empty_like(logits)
-        if T:
-            _lib.dg_moe_route_backward(grad_weights, logits, ids, g, T, E, k, s, int(renorm), scale, _TYPES[logits.dtype])
+    dev = logits.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_route_backward(grad_weights, logits, ids, score, renorm, scale)
+    g = torch.empty_like(logits)
+    if T:
+        _lib.dg_moe_route_backward(grad_weights, logits, ids, g, T, E, k, s, int(renorm), scale, _TYPES[logits.dtype],
+                                   _raw_stream(dev))
     return g
 
 
@@ -360,11 +386,14 @@ def moe_layout_contiguous(ids, G, M_sum=None, stream=None):
     if M_sum is None:
         M_sum = (T * k + 127 * min(G, T * k) + 127) // 128 * 128
     _check_sizes(G, M_sum)
-    with _on(ids.get_device(), stream):
-        dst = torch.empty_like(ids)
-        layout = ids.new_empty(M_sum)
-        ks = ids.new_empty(G)
-        _lib.dg_moe_layout_contiguous(ids, dst, layout, ks, T, k, G, M_sum)
+    dev = ids.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_layout_contiguous(ids, G, M_sum)
+    dst = torch.empty_like(ids)
+    layout = ids.new_empty(M_sum)
+    ks = ids.new_empty(G)
+    _lib.dg_moe_layout_contiguous(ids, dst, layout, ks, T, k, G, M_sum, _raw_stream(dev))
     return dst, layout, ks
 
 
@@ -373,10 +402,13 @@ def moe_layout_masked(ids, G, M_max, stream=None):
     (dst_rows int32 [T,k] with row g·M_max + i for expert g's i-th token, masked_m int32 [G])."""
     T, k = _check_2d("ids", ids, torch.int32)
     _check_sizes(G, M_max)
-    with _on(ids.get_device(), stream):
-        dst = torch.empty_like(ids)
-        masked_m = ids.new_empty(G)
-        _lib.dg_moe_layout_masked(ids, dst, masked_m, T, k, G, M_max)
+    dev = ids.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_layout_masked(ids, G, M_max)
+    dst = torch.empty_like(ids)
+    masked_m = ids.new_empty(G)
+    _lib.dg_moe_layout_masked(ids, dst, masked_m, T, k, G, M_max, _raw_stream(dev))
     return dst, masked_m
 
 
@@ -393,12 +425,15 @@ def cast_per_token_scatter_topk(x, dst_rows, M, G=1, out=None, stream=None):
     if out is not None:
         _check("out[0]", out[0], (G * M, K), torch.uint8, x.get_device())
         _check("out[1]", out[1], (G, K // 128, _pad4(M)), torch.float32, x.get_device())
-    with _on(x.get_device(), stream):
-        q, sfa = out if out is not None else (
-            x.new_zeros((G * M, K), dtype=torch.uint8),
-            torch.zeros((G, K // 128, _pad4(M)), dtype=torch.float32, device=x.device))
-        if T and k and G * M:
-            _lib.dg_cast_fp8_per_token_scatter_topk(x, dst_rows, q, sfa, T, k, G, M, K)
+    dev = x.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return cast_per_token_scatter_topk(x, dst_rows, M, G, out)
+    q, sfa = out if out is not None else (
+        x.new_zeros((G * M, K), dtype=torch.uint8),
+        torch.zeros((G, K // 128, _pad4(M)), dtype=torch.float32, device=x.device))
+    if T and k and G * M:
+        _lib.dg_cast_fp8_per_token_scatter_topk(x, dst_rows, q, sfa, T, k, G, M, K, _raw_stream(dev))
     return q, sfa
 
 
@@ -424,10 +459,13 @@ def moe_combine(d, dst_rows, weights=None, c=None, out=None, stream=None):
         _check("c", c, (T, N), torch.bfloat16, d.get_device())
     if out is not None:
         _check("out", out, (T, N), torch.bfloat16, d.get_device())
-    with _on(d.get_device(), stream):
-        y = out if out is not None else d.new_empty((T, N))
-        if T:
-            _lib.dg_moe_combine(d, dst_rows, weights, c, y, T, k, N, R)
+    dev = d.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_combine(d, dst_rows, weights, c, out)
+    y = out if out is not None else d.new_empty((T, N))
+    if T:
+        _lib.dg_moe_combine(d, dst_rows, weights, c, y, T, k, N, R, _raw_stream(dev))
     return y
 
 
@@ -441,9 +479,12 @@ def moe_combine_backward(grad_y, d, dst_rows, weights=None, grouped_layout=None,
         _check("weights", weights, (T, k), torch.float32, d.get_device())
     if grouped_layout is not None:
         _check("grouped_layout", grouped_layout, (R,), torch.int32, d.get_device())
-    with _on(d.get_device(), stream):
-        gd = (torch.zeros_like if grouped_layout is None else torch.empty_like)(d)
-        gw = d.new_empty((T, k), dtype=torch.float32)
-        if T or (R and grouped_layout is not None):
-            _lib.dg_moe_combine_backward(grad_y, d, dst_rows, weights, grouped_layout, gd, gw, T, k, N, R)
+    dev = d.get_device()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_combine_backward(grad_y, d, dst_rows, weights, grouped_layout)
+    gd = (torch.zeros_like if grouped_layout is None else torch.empty_like)(d)
+    gw = d.new_empty((T, k), dtype=torch.float32)
+    if T or (R and grouped_layout is not None):
+        _lib.dg_moe_combine_backward(grad_y, d, dst_rows, weights, grouped_layout, gd, gw, T, k, N, R, _raw_stream(dev))
     return gd, gw

@@ -46,7 +46,7 @@ def cuda(t):
 
 
 SHAPES = [(1, 1), (3, 2), (2, 7), (9, 64), (5, 129), (17, 1000), (300, 1001), (777, 1001), (1, 7168), (33, 2048), (311, 7168),
-          (7, 4097), (2, 8191), (600, 24), (1000, 128), (333, 256), (700, 512), (3, 16384), (310, 16384), (301, 12296), (2, 20001), (2, 32768), (299, 260)]
+          (7, 4097), (2, 8191), (600, 24), (1000, 128), (333, 256), (700, 512), (3, 16384), (310, 16384), (301, 12296), (2, 20001), (2, 32768), (300, 32768), (299, 260), (3, 9001), (300, 9001), (2, 8540), (297, 20000)]
 
 
 @pytest.mark.parametrize("T,K", SHAPES)
