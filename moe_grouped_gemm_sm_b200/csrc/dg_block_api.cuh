@@ -197,10 +197,10 @@ dg_status check_route(int T, int E, int k, int score, int dtype) {
     return DG_OK;
 }
 
-// A warp takes a token; warps beyond 32 an SM take further ones (they keep the bias in registers).
+// A warp takes a token; the warps of ROUTE_BLOCKS blocks an SM take further ones (they keep the bias in registers).
 template <typename LT>
 dg_status run_route(const dg::RouteParams &p, int sm_count, cudaStream_t st) {
-    const int blocks = std::min((p.T + dg::ROUTE_WARPS - 1) / dg::ROUTE_WARPS, sm_count * 32 / dg::ROUTE_WARPS);
+    const int blocks = std::min((p.T + dg::ROUTE_WARPS - 1) / dg::ROUTE_WARPS, sm_count * dg::ROUTE_BLOCKS);
     Launch ln(dim3(static_cast<unsigned>(blocks), 1, 1), dim3(32 * dg::ROUTE_WARPS, 1, 1), 0, st);
     const int per_lane = (p.E + 31) / 32;
     if (per_lane <= 1) return from_cuda(cudaLaunchKernelEx(&ln.cfg, dg::route_kernel<LT, 1>, p));

@@ -21,7 +21,8 @@
 namespace dg {
 
 enum : int { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1 };
-constexpr int ROUTE_WARPS = 4;   // tokens per block
+constexpr int ROUTE_WARPS = 4;    // tokens per block
+constexpr int ROUTE_BLOCKS = 7;   // blocks per SM (for up to 256 experts)
 constexpr int ROUTE_MAX_E = 1024, ROUTE_MAX_K = 32, ROUTE_MAX_GROUPS = 32;
 
 struct RouteParams {
@@ -257,9 +258,9 @@ __device__ __forceinline__ void sort_falling(float (&v)[N]) {
 // their 64-bit values, and groups at the border likewise. Neighbours with the same logit and the
 // same bias are equal in truth and need no second look. With N(0,1.5) logits over 256 experts that
 // is about 40 of 16384 tokens.
-// Bound by instructions (1030 a token and warp with 8 groups over 256 experts, 63 % of the issue slots used): 16384 tokens
-// take 23.5 us, 65536 80 us; every value in 64 bits took 122 us. Traffic alone would be 2.7 us for 16384. 8 blocks an SM
-// (64 registers, some spilled) are faster than 6 or 4 without spills: 80 against 96 us for 65536 tokens.
+// Bound by instructions (some 880 a token and warp with 8 groups over 256 experts): 16384 tokens take 21 us, 65536
+// 71 us; every value in 64 bits took 122 us for 16384. Traffic alone would be 2.7 us. 7 blocks an SM (72 registers)
+// against 8, 6 and 5: 71, 74, 72 and 76 us for 65536 tokens.
 template <typename LT, int EPL>
 __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&b)[EPL], int t, int lane) {
     const bool softmax = p.score == SCORE_SOFTMAX, by_logit = p.bias == nullptr;
@@ -318,7 +319,38 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
     const float tol_score = softmax ? top * 0x1p-17f : 0x1p-20f;
     if (p.groups > 1) {
         float a1 = -CUDART_INF_F, a2 = -CUDART_INF_F;   // lane g: the two largest of group g
-        if (p.rows_per_group) {
+        if (p.rows_per_group == 1 && p.groups == EPL) {
+            // A register a group: each step over the lanes halves the groups that a lane goes on with, until a lane
+            // has the two largest of one group among its lanes; then lane g fetches those of group g.
+            float b1[EPL], b2[EPL];
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                b1[i] = c[i];
+                b2[i] = -CUDART_INF_F;
+            }
+#pragma unroll
+            for (int o = 16, m = EPL / 2; o >= 1; o >>= 1, m >>= 1) {
+                const bool up = (lane & o) != 0;
+                if (m >= 1) {
+#pragma unroll
+                    for (int h = 0; h < m; ++h) {
+                        const float v1 = __shfl_xor_sync(0xFFFFFFFFu, up ? b1[h] : b1[h + m], o);
+                        const float v2 = __shfl_xor_sync(0xFFFFFFFFu, up ? b2[h] : b2[h + m], o);
+                        const float m1 = up ? b1[h + m] : b1[h], m2 = up ? b2[h + m] : b2[h];
+                        b2[h] = fmaxf(fminf(m1, v1), fmaxf(m2, v2));
+                        b1[h] = fmaxf(m1, v1);
+                    }
+                } else {
+                    const float v1 = __shfl_xor_sync(0xFFFFFFFFu, b1[0], o), v2 = __shfl_xor_sync(0xFFFFFFFFu, b2[0], o);
+                    b2[0] = fmaxf(fminf(b1[0], v1), fmaxf(b2[0], v2));
+                    b1[0] = fmaxf(b1[0], v1);
+                }
+            }
+            const int from = lane * (32 / EPL) & 31;
+            a1 = __shfl_sync(0xFFFFFFFFu, b1[0], from);
+            a2 = __shfl_sync(0xFFFFFFFFu, b2[0], from);
+            if (lane >= EPL) a1 = a2 = -CUDART_INF_F;
+        } else if (p.rows_per_group) {
             // groups of whole registers: first the two largest of each register, in lane i
             float r1 = -CUDART_INF_F, r2 = -CUDART_INF_F;
 #pragma unroll
@@ -334,17 +366,12 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
                     r2 = m2;
                 }
             }
-            if (p.rows_per_group == 1) {
-                a1 = r1;
-                a2 = r2;
-            } else {
-                for (int q = 0; q < p.rows_per_group; ++q) {
-                    const int from = lane * p.rows_per_group + q;
-                    const float v1 = __shfl_sync(0xFFFFFFFFu, r1, from & 31), v2 = __shfl_sync(0xFFFFFFFFu, r2, from & 31);
-                    if (lane < p.groups) {
-                        a2 = fmaxf(fminf(a1, v1), fmaxf(a2, v2));
-                        a1 = fmaxf(a1, v1);
-                    }
+            for (int q = 0; q < p.rows_per_group; ++q) {
+                const int from = lane * p.rows_per_group + q;
+                const float v1 = __shfl_sync(0xFFFFFFFFu, r1, from & 31), v2 = __shfl_sync(0xFFFFFFFFu, r2, from & 31);
+                if (lane < p.groups) {
+                    a2 = fmaxf(fminf(a1, v1), fmaxf(a2, v2));
+                    a1 = fmaxf(a1, v1);
                 }
             }
         } else {
@@ -374,9 +401,18 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
         }
         const float mine = p.group_top == 2 && a2 > -CUDART_INF_F ? a1 + a2 : a1;
         int rank = 0;
-        for (int h = 0; h < p.groups; ++h) {
-            const float v = __shfl_sync(0xFFFFFFFFu, mine, h);
-            rank += (v > mine || (v == mine && h < lane)) ? 1 : 0;
+        if (p.groups == 8) {
+            // among lanes 0 .. 7 (the others rank among themselves and are not asked)
+#pragma unroll
+            for (int h = 1; h < 8; ++h) {
+                const float v = __shfl_xor_sync(0xFFFFFFFFu, mine, h);
+                rank += ((lane ^ h) < lane ? v >= mine : v > mine) ? 1 : 0;
+            }
+        } else {
+            for (int h = 0; h < p.groups; ++h) {
+                const float v = __shfl_sync(0xFFFFFFFFu, mine, h);
+                rank += (v > mine || (v == mine && h < lane)) ? 1 : 0;
+            }
         }
         const bool keep = lane < p.groups && rank < p.topk_groups;
         uint32_t kept = __ballot_sync(0xFFFFFFFFu, keep);
@@ -428,16 +464,18 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
         sort_falling<EPL>(c);
     }
     float v = -CUDART_INF_F;   // lane j: the j-th largest
-    int from = 0;
+    uint32_t from = 0;         // and the lanes that had it; the lowest one's is taken
+    const uint32_t below = (1u << lane) - 1u;
     // lane `at` takes the largest value that is left, and its lane's values move up
     const auto take = [&](int at) {
         const float m = redux_max(c[0]);
-        const int f = __ffs(__ballot_sync(0xFFFFFFFFu, c[0] == m)) - 1;
+        const bool mine = c[0] == m;
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, mine);
         if (lane == at) {
             v = m;
-            from = f;
+            from = have;
         }
-        if (lane == f) {
+        if (mine && (have & below) == 0) {
 #pragma unroll
             for (int i = 0; i + 1 < EPL; ++i) c[i] = c[i + 1];
             c[EPL - 1] = -CUDART_INF_F;
@@ -447,7 +485,8 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
     const auto expert = [&] {
         const uint32_t u = __float_as_uint(v);
         return v > -CUDART_INF_F
-                   ? static_cast<int>((~static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) ^ u) & (EPL - 1)) * 32 + from
+                   ? static_cast<int>((~static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) ^ u) & (EPL - 1)) * 32 +
+                         __ffs(from) - 1
                    : -1;
     };
     int id = expert(), place = lane;
@@ -496,7 +535,7 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
 // Tokens in batches of up to 32 per warp, then the batch's tokens that are done again: the 64-bit
 // form is a call, and nothing of the fp32 form has to live across it.
 template <typename LT, int EPL>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS, EPL <= 8 ? 8 : 1) route_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(32 * ROUTE_WARPS, EPL <= 8 ? ROUTE_BLOCKS : 1) route_kernel(const __grid_constant__ RouteParams p) {
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, step = gridDim.x * ROUTE_WARPS;
