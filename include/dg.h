@@ -261,7 +261,8 @@ DG_API dg_status dg_cast_fp8_per_block_ue8m0(const void *x, void *q, uint32_t *s
  *   not written). T % 128 == 0, C % 8 == 0, else DG_ERR_INVALID_ARG. */
 DG_API dg_status dg_cast_fp8_per_channel(const void *x, void *q, float *sf, int T, int C, void *stream);
 
-/* Element types of the operators below that take more than one. */
+/* Element types of the operators below that take more than one. Their row counts T are at most 2^30; outputs
+ * may overlap inputs only where it is said. */
 typedef enum dg_dtype { DG_BF16 = 0, DG_FP32 = 1 } dg_dtype;
 
 /* Layer norm (rms = 0) or RMS norm (rms != 0) over the K elements of each row, with the

@@ -1,5 +1,7 @@
 """Rows of the grouped layouts, the top-k dispatch cast and the weighted combine with its gradient, each
 against a plain implementation; then all of them together around the framework's grouped GEMMs."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -405,6 +407,44 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, ref))
     assert _lib.dg_get_device_error() == _lib.DG_OK
+
+
+def test_two_threads_at_once():
+    """Calls from two host threads, each on a stream of its own, give what one thread's calls give."""
+    T, K, G, k = 300, 512, 32, 4
+    gen = torch.Generator().manual_seed(12)
+    data = [(torch.randn(T, K, generator=gen).bfloat16().cuda(), torch.randn(T, G, generator=gen).cuda()) for _ in range(2)]
+
+    def step(x, logits):
+        h, mean, rstd = ops.layer_norm(x, stats=True)
+        wt, ids = ops.moe_route(logits, k, score="sigmoid")
+        dst, layout, ks = ops.moe_layout_contiguous(ids, G)
+        q, sfa = ops.cast_per_token_scatter_topk(h, dst, layout.numel())
+        d = torch.zeros(layout.numel(), K, dtype=torch.bfloat16, device="cuda")
+        d[dst.long().reshape(-1)] = h.repeat_interleave(k, 0)
+        y = ops.moe_combine(d, dst, wt, c=x)
+        gd, gw = ops.moe_combine_backward(x, d, dst, wt, grouped_layout=layout)
+        gl = ops.moe_route_backward(gw, logits, ids, score="sigmoid")
+        dx, _, db = ops.layer_norm_backward(y, x, None, mean, rstd)
+        return h, wt, ids, dst, layout, ks, q, sfa, y, gw, gl, dx, db
+    refs = [step(*v) for v in data]
+    torch.cuda.synchronize()
+    streams, bad = [torch.cuda.Stream() for _ in data], []
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(20):
+                out = step(*data[i])
+                streams[i].synchronize()
+                if not all(torch.equal(p, q) for p, q in zip(out, refs[i])):
+                    bad.append(i)
+                streams[i].synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and _lib.dg_get_device_error() == _lib.DG_OK
 
 
 def test_refusals():
