@@ -276,7 +276,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, stats=False, out=
     mean = rstd = None
     if stats:
         rstd = x.new_empty(T, dtype=torch.float32)
-        mean = None if rms else x.new_empty(T, dtype=torch.float32)
+        mean = None if rms else torch.empty_like(rstd)
     if T:
         _lib.dg_layer_norm(x, weight, bias, y, None, None, mean, rstd, T, K, eps, int(rms), _TYPES[x.dtype], w_type,
                            _raw_stream(dev))
@@ -293,7 +293,7 @@ def layer_norm_cast(x, weight=None, bias=None, eps=1e-5, rms=False, stream=None)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return layer_norm_cast(x, weight, bias, eps, rms)
-    q = x.new_empty((T, K), dtype=torch.uint8)
+    q = torch.empty_like(x, dtype=torch.uint8)
     sfa = (x.new_zeros if T % 4 else x.new_empty)((K // 128, _pad4(T)), dtype=torch.float32)
     if T:
         _lib.dg_layer_norm(x, weight, bias, None, q, sfa, None, None, T, K, eps, int(rms), _TYPES[x.dtype], w_type,
@@ -318,7 +318,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, rms=False, stream=
         with _on(dev, stream):
             return layer_norm_backward(dy, x, weight, mean, rstd, bias, rms)
     dx = torch.empty_like(x)
-    dw = x.new_empty(K, dtype=torch.float32) if weight is not None else None
+    dw = torch.empty_like(weight, dtype=torch.float32) if weight is not None else None
     db = x.new_empty(K, dtype=torch.float32) if bias else None
     if T == 0:
         for g in (dw, db):
@@ -353,7 +353,7 @@ def moe_route(logits, k, bias=None, groups=1, topk_groups=1, group_top=1, score=
         with _on(dev, stream):
             return moe_route(logits, k, bias, groups, topk_groups, group_top, score, renorm, scale)
     ids = logits.new_empty((T, k), dtype=torch.int32)
-    weights = logits.new_empty((T, k), dtype=torch.float32)
+    weights = torch.empty_like(ids, dtype=torch.float32)
     if T:
         _lib.dg_moe_route(logits, bias, ids, weights, T, E, k, groups, topk_groups, group_top, s, int(renorm), scale,
                           _TYPES[logits.dtype], _raw_stream(dev))
@@ -463,7 +463,7 @@ def moe_combine(d, dst_rows, weights=None, c=None, out=None, stream=None):
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return moe_combine(d, dst_rows, weights, c, out)
-    y = out if out is not None else d.new_empty((T, N))
+    y = out if out is not None else d.new_empty((T, N)) if c is None else torch.empty_like(c)
     if T:
         _lib.dg_moe_combine(d, dst_rows, weights, c, y, T, k, N, R, _raw_stream(dev))
     return y
@@ -484,7 +484,7 @@ def moe_combine_backward(grad_y, d, dst_rows, weights=None, grouped_layout=None,
         with _on(dev, stream):
             return moe_combine_backward(grad_y, d, dst_rows, weights, grouped_layout)
     gd = (torch.zeros_like if grouped_layout is None else torch.empty_like)(d)
-    gw = d.new_empty((T, k), dtype=torch.float32)
+    gw = torch.empty_like(dst_rows, dtype=torch.float32)
     if T or (R and grouped_layout is not None):
         _lib.dg_moe_combine_backward(grad_y, d, dst_rows, weights, grouped_layout, gd, gw, T, k, N, R, _raw_stream(dev))
     return gd, gw
