@@ -63,11 +63,14 @@ NormRingShape norm_ring_shape(int T, int K, int x_type, int tensors) {
     s.teams = s.threads == 32 ? 4 : 1;
     if (s.cols && K == s.n * s.threads) s.cols = dg::COLS_EXACT;
     const size_t row = static_cast<size_t>(dg::NORM_STAGES) * tensors * (s.cols ? K : (K + 2 * c - 2) / c * c) * size;
-    // two rows a step where the rings of the blocks that the threads allow still fit an SM: 8192 x 4096 fp32
-    // backward takes 86 us with one block of two rows an SM
+    // Two rows a step where the rings of the blocks that the threads allow still fit an SM (8192 x 4096 fp32 backward
+    // takes 86 us with one block of two rows an SM and 71 with two of one row). Backward, a single row stays in registers
+    // between its sums and dx, and that beats two rows unless the columns are exact: 8192 x 7168 bf16 68 us by two and 72
+    // by one, 8192 x 1000 24 and 19, 8192 x 3001 73 and 62.
     const int most = std::max(1, dg::NORM_RING_THREADS / (s.threads * s.teams));
     const size_t ring = static_cast<size_t>(kNormRing), sm = static_cast<size_t>(220 << 10);
     s.r = s.n <= 16 && 2 * row * s.teams * most <= sm && 2 * row <= ring ? 2 : 1;
+    if (tensors == 2 && s.n == 16 && s.cols != dg::COLS_EXACT) s.r = 1;
     if (s.threads > dg::NORM_RING_THREADS || (s.n == 32 && !s.cols) || s.r * row > ring) return s;
     s.smem = s.teams * s.r * row;
     const int per_sm = std::max(1, std::min(most, static_cast<int>(sm / s.smem)));
@@ -168,11 +171,9 @@ dg_status run_layer_norm_backward(dg::NormBackParams p, int x_type, cudaStream_t
             s = sh.r == 2 ? launch_norm_backward<XT, WT, 16, 2, dg::COLS_EXACT>(p, sh, st)
                           : launch_norm_backward<XT, WT, 16, 1, dg::COLS_EXACT>(p, sh, st);
         else if (sh.cols == dg::COLS_VECTORS)
-            s = sh.r == 2 ? launch_norm_backward<XT, WT, 16, 2, dg::COLS_VECTORS>(p, sh, st)
-                          : launch_norm_backward<XT, WT, 16, 1, dg::COLS_VECTORS>(p, sh, st);
+            s = launch_norm_backward<XT, WT, 16, 1, dg::COLS_VECTORS>(p, sh, st);
         else
-            s = sh.r == 2 ? launch_norm_backward<XT, WT, 16, 2, dg::COLS_SINGLE>(p, sh, st)
-                          : launch_norm_backward<XT, WT, 16, 1, dg::COLS_SINGLE>(p, sh, st);
+            s = launch_norm_backward<XT, WT, 16, 1, dg::COLS_SINGLE>(p, sh, st);
     } else {
         constexpr int V = 16 / static_cast<int>(sizeof(XT));
         if (p.K % V != 0)

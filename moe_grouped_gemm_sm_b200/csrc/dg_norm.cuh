@@ -655,6 +655,7 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(
     const float inv_k = 1.f / static_cast<float>(K);
     const Pair zero = pair(0.f, 0.f);
     constexpr bool KEEP = N <= 16;   // w in registers, or read again (from L1) for every row
+    constexpr bool HOLD = R == 1 && N <= 16;   // the row stays in registers across its sums
     Pair w[H], aw[H], ab[H];
     const auto parameters = [&] {
         if (p.w) {
@@ -702,6 +703,7 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(
             r[q] = __shfl_sync(0xFFFFFFFFu, rstd32, (n * R + q) & 31);
         }
         float sums[2 * R];
+        Pair hx[HOLD ? H : 1], hd[HOLD ? H : 1];
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             sums[2 * q] = sums[2 * q + 1] = 0.f;
@@ -711,6 +713,13 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(
                 if constexpr (!KEEP) parameters();
                 cols.load(ring + (stage * R + q) * 2 * pitch + off, fx);
                 cols.load(ring + ((stage * R + q) * 2 + 1) * pitch + off, fd);
+                if constexpr (HOLD) {
+#pragma unroll
+                    for (int e = 0; e < H; ++e) {
+                        hx[e] = fx[e];
+                        hd[e] = fd[e];
+                    }
+                }
                 const Pair c = pair(-mu[q], -mu[q]);
                 Pair s1 = zero, s2 = zero;
 #pragma unroll
@@ -748,10 +757,18 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(
         for (int q = 0; q < R; ++q) {
             if (row + q * step < p.T) {
                 const size_t at = static_cast<size_t>(row + q * step) * K;
-                Pair fx[H], fd[H];   // read again: they need not live across the sums
+                Pair fx[H], fd[H];   // two rows are read again: they would not fit across the sums
                 if constexpr (!KEEP) parameters();
-                cols.load(ring + (stage * R + q) * 2 * pitch + cols.offset(at), fx);
-                cols.load(ring + ((stage * R + q) * 2 + 1) * pitch + cols.offset(at), fd);
+                if constexpr (HOLD) {
+#pragma unroll
+                    for (int e = 0; e < H; ++e) {
+                        fx[e] = hx[e];
+                        fd[e] = hd[e];
+                    }
+                } else {
+                    cols.load(ring + (stage * R + q) * 2 * pitch + cols.offset(at), fx);
+                    cols.load(ring + ((stage * R + q) * 2 + 1) * pitch + cols.offset(at), fd);
+                }
                 const float rq = r[q], b0 = p.mean ? -rq * (sums[2 * q] * inv_k) : 0.f;
                 const float a0 = -rq * (rq * (sums[2 * q + 1] * inv_k));   // -r·c2, c2 = r·mean(u·d)
                 const Pair c = pair(-mu[q], -mu[q]), rr = pair(rq, rq), pa = pair(a0, a0), pb = pair(b0, b0);
