@@ -144,8 +144,8 @@ __device__ __noinline__ double route_group_f64(const RouteParams &p, const LT *r
 
 // One token by a warp with every value that decides the choice in 64 bits; lane l holds the
 // experts l, l + 32, .... Taken for k > 30 and where more than 31 candidates lie too close together
-// for fp32 (rows of equal fp32 logits, say). Rolled loops over a local array keep the code short: it is rarely in the instruction
-// cache, and unrolled it took 12 us for a single token, most of it fetching instructions.
+// for fp32 (rows of equal fp32 logits, say). Rolled loops over a local array keep the code short: it
+// is rarely in the instruction cache (unrolled or not, a token takes 12 to 14 us alone).
 template <typename LT>
 __device__ __noinline__ void route_token_f64(const RouteParams &p, int t) {
     const int lane = threadIdx.x & 31, n = (p.E + 31) / 32;
