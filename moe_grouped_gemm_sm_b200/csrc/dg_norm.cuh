@@ -10,6 +10,7 @@
 // Sums, statistics and the gradients of w and b are fp32; a result is rounded once, to x's type.
 #pragma once
 #include <cuda_bf16.h>
+#include <math_constants.h>
 #include <stdint.h>
 
 #include "dg_cast.cuh"
@@ -142,6 +143,15 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     float s = 0.f;
     for (int i = 0; i < nw; ++i) s += red[i];
     return s;
+}
+
+// s / n from inv = 1/n. The product with the rounded reciprocal alone may miss the quotient by a unit in the last
+// place, and a row of equal values would then have a deviation: 7168 times 3 gave a mean of 3.0000002. The
+// remainder s - q·n is exact in one fma, and the second one adds what is missing (Markstein's correction of a
+// quotient): three instructions, once a row. A quotient that is not finite stays as it is.
+__device__ __forceinline__ float mean_of(float s, float n, float inv) {
+    const float q = s * inv;
+    return fabsf(q) <= CUDART_MAX_NORMAL_F ? fmaf(fmaf(-q, n, s), inv, q) : q;
 }
 
 constexpr int NORM_MAX_THREADS = 1024, NORM_DX_MAX_THREADS = 512;   // threads of a row
@@ -395,9 +405,11 @@ __device__ __forceinline__ void ring_step(F refill) {
     }
 }
 
-// The mean square is taken about the warp's own mean and moved to the row's mean afterwards (as exact
-// as about the row's mean), so the R rows cost one barrier.
-// 8192 x 7168 bf16: 49 us, 73 % of the copy rate (a block a row, the kernel above: 62); fp32 80 us, 90 %. What is left
+// The mean square is taken about the warp's own mean and moved to the row's mean afterwards, so the R rows cost one
+// barrier. (Both means are sums divided by their count to the last place, so a row of equal values has deviation 0, as
+// in the kernel above. The rounding of the warp's mean enters the mean square squared, and times its distance from the
+// row's mean.)
+// 8192 x 7168 bf16: 50 us, 72 % of the copy rate (a block a row, the kernel above: 62); fp32 80 us, 90 %. What is left
 // in bf16 is instructions: 14 warps an SM, which the registers allow, issue in half of the cycles.
 template <typename XT, typename WT, int N, int R, int COLS>
 __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_ring_kernel(const __grid_constant__ NormParams p) {
@@ -432,7 +444,8 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_ring_kernel(cons
     };
     if constexpr (KEEP) parameters();
     const int count = cols.count(tid >> 5), count_of_lane = lane < nw ? cols.count(lane) : 0;
-    const float inv_count = count ? 1.f / static_cast<float>(count) : 0.f, inv_k = 1.f / static_cast<float>(K);
+    const float own = static_cast<float>(count), inv_count = count ? 1.f / own : 0.f;
+    const float fk = static_cast<float>(K), inv_k = 1.f / fk;
     const auto fetch = [&](int first, int stage) {
 #pragma unroll
         for (int q = 0; q < R; ++q)
@@ -469,10 +482,10 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_ring_kernel(cons
         if (!p.rms) {   // the warp's means
             if constexpr (R == 2) {
                 const float2 s = warp_sum2(mu[0], mu[1]);
-                mu[0] = s.x * inv_count;
-                mu[1] = s.y * inv_count;
+                mu[0] = mean_of(s.x, own, inv_count);
+                mu[1] = mean_of(s.y, own, inv_count);
             } else {
-                mu[0] = warp_sum(mu[0]) * inv_count;
+                mu[0] = mean_of(warp_sum(mu[0]), own, inv_count);
             }
         }
 #pragma unroll
@@ -499,8 +512,8 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_ring_kernel(cons
             }
             if (!p.rms) {
                 const float2 s = R == 2 ? warp_sum2(a[0], a[R - 1]) : make_float2(warp_sum(a[0]), 0.f);
-                mu[0] = s.x * inv_k;
-                if (R == 2) mu[R - 1] = s.y * inv_k;
+                mu[0] = mean_of(s.x, fk, inv_k);
+                if (R == 2) mu[R - 1] = mean_of(s.y, fk, inv_k);
             }
 #pragma unroll
             for (int q = 0; q < R; ++q) a[q] = p.rms ? v[q].y : fmaf(c * (v[q].x - mu[q]), v[q].x - mu[q], v[q].y);

@@ -287,3 +287,21 @@ def test_more_than_2_to_31_elements():
     assert ((dx[-5:].cpu().double() - rx).abs() <= tx + 2.0 ** -8 * (rx.abs() + tx)).all()
     assert not dx[:T - 5].any()
     assert ((dw.cpu().double() - rw).abs() <= tw).all() and ((db.cpu().double() - rb).abs() <= tb).all()
+
+
+@pytest.mark.parametrize("K", [200, 768, 1000, 1001, 7168, 8191, 12288, 12296])
+@pytest.mark.parametrize("T", [4, 300])
+@pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
+def test_rows_of_one_value_have_no_deviation(T, K, xt):
+    """Rows of one value: its mean is the value, its deviation 0 and the result the bias, exactly, however many rows
+    share the call. The values have 8 bits at most and K <= 2^14, so every sum of them is exact in fp32."""
+    values = torch.tensor([3.0, 1000.0, -49920.0, 0.375]).repeat(T // 4)
+    x = values[:, None].expand(T, K).to(xt).contiguous()
+    _, w, b = make(1, K, xt, torch.float32, False, seed=12)
+    y, mean, rstd = ops.layer_norm(cuda(x), cuda(w), cuda(b), stats=True)
+    assert torch.equal(mean.cpu(), values)
+    assert ((rstd.cpu().double() - 1e-5 ** -0.5).abs() <= 4 * U * 1e-5 ** -0.5).all()   # eps and the root: 2 ulp
+    assert torch.equal(y.cpu(), b.to(xt).expand(T, K))
+    if K % 128 == 0:
+        q, sfa = ops.layer_norm_cast(cuda(x))
+        assert not q.any() and (sfa[:, :T] == 1).all()
