@@ -341,6 +341,8 @@ dg_status dg_layer_norm_backward(const void *dy, const void *x, const void *weig
     p.db = db;
     p.T = T;
     p.K = K;
+    p.len = static_cast<float>(K);
+    p.inv_len = 1.f / p.len;
     if (x_type == DG_BF16)
         return w_type == DG_BF16 ? run_layer_norm_backward<__nv_bfloat16, __nv_bfloat16>(p, x_type, st)
                                  : run_layer_norm_backward<__nv_bfloat16, float>(p, x_type, st);

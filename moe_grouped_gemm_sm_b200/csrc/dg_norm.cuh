@@ -10,7 +10,6 @@
 // Sums, statistics and the gradients of w and b are fp32; a result is rounded once, to x's type.
 #pragma once
 #include <cuda_bf16.h>
-#include <math_constants.h>
 #include <stdint.h>
 
 #include "dg_cast.cuh"
@@ -148,10 +147,10 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 // s / n from inv = 1/n. The product with the rounded reciprocal alone may miss the quotient by a unit in the last
 // place, and a row of equal values would then have a deviation: 7168 times 3 gave a mean of 3.0000002. The
 // remainder s - q·n is exact in one fma, and the second one adds what is missing (Markstein's correction of a
-// quotient): three instructions, once a row. A quotient that is not finite stays as it is.
+// quotient): three instructions, once a row. A sum that is not finite gives NaN: its row has no finite result anyway.
 __device__ __forceinline__ float mean_of(float s, float n, float inv) {
     const float q = s * inv;
-    return fabsf(q) <= CUDART_MAX_NORMAL_F ? fmaf(fmaf(-q, n, s), inv, q) : q;
+    return fmaf(fmaf(-q, n, s), inv, q);
 }
 
 constexpr int NORM_MAX_THREADS = 1024, NORM_DX_MAX_THREADS = 512;   // threads of a row
@@ -563,6 +562,7 @@ struct NormBackParams {
     float *part;                // [parts][2 or 1][K] column sums (dw, then db)
     float *dw, *db;             // may be NULL
     int T, K, parts;
+    float len, inv_len;         // K and 1/K: operands from here cost the row kernel no registers
 };
 
 // Long rows: dx of one row per blockDim.x threads, laid out as in the forward kernel.
@@ -645,7 +645,8 @@ __global__ void __launch_bounds__(256) layer_norm_dwdb_kernel(const NormBackPara
 // dx, and the sums of dw and db, in one pass over dy and x: HBM-bound (three tensors of T·K). Teams, columns
 // and the ring are those of the forward kernel, with rows of x and dy side by side; a thread's columns' dw
 // and db stay in registers to the end, and R rows cost one barrier for their sums of u and u·(x - mu).
-// dx = (dy·r)·w - r·c1 - xh·(r·c2) with c1 = mean(u), c2 = r·mean(u·(x - mu)).
+// dx = (dy·r)·w - r·c1 - xh·(r·c2) with c1 = mean(u), c2 = r·mean(u·(x - mu)). c1 is divided to the last place: where
+// all u of a row are equal it has to cancel them, and an ulp left over would be multiplied by r.
 // The teams' sums meet in shared memory and go to part[blockIdx.x] in a fixed order.
 // 8192 x 7168 bf16, with the parts' sum: 70 us, 77 % of the copy rate; fp32 123 us, 88 %. A dx kernel and a column kernel
 // took 250 us. 8 columns a thread (twice the threads, half the registers) spill: 127 to 142 us.
@@ -665,7 +666,6 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(
     const Cols cols(K);
     const XT *x = static_cast<const XT *>(p.x), *dy = static_cast<const XT *>(p.dy);
     XT *ring = reinterpret_cast<XT *>(s_norm) + static_cast<size_t>(threadIdx.y) * NORM_STAGES * R * 2 * pitch;
-    const float inv_k = 1.f / static_cast<float>(K);
     const Pair zero = pair(0.f, 0.f);
     constexpr bool KEEP = N <= 16;   // w in registers, or read again (from L1) for every row
     constexpr bool HOLD = R == 1 && N <= 16;   // the row stays in registers across its sums
@@ -746,6 +746,7 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(
                 sums[2 * q + 1] = h2.x + h2.y;
             }
         }
+        float means[2 * R];   // of u and of u·(x - mu)
         if constexpr (R == 2) {
             float s = warp_sum4_spread(make_float4(sums[0], sums[1], sums[2], sums[3]));
             if (nt > 32) {
@@ -753,8 +754,9 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(
                 __syncthreads();   // the other half of s_red is free: all have left the last rows' sums
                 s = warp_sum4_spread(lane < nt / 32 ? s_red[n & 1][lane] : make_float4(0.f, 0.f, 0.f, 0.f));
             }
+            s = mean_of(s, p.len, p.inv_len);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sums[i] = __shfl_sync(0xFFFFFFFFu, s, 8 * i);
+            for (int i = 0; i < 4; ++i) means[i] = __shfl_sync(0xFFFFFFFFu, s, 8 * i);
         } else {
             float2 s = warp_sum2(sums[0], sums[1]);
             if (nt > 32) {
@@ -763,8 +765,9 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(
                 const float4 v = lane < nt / 32 ? s_red[n & 1][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
                 s = warp_sum2(v.x, v.y);
             }
-            sums[0] = s.x;
-            sums[1] = s.y;
+            // mean_of, written out: the call's order of instructions costs odd rows 5 % (8192 x 4097 120 us, so 115)
+            means[0] = fmaf(fmaf(-(s.x * p.inv_len), p.len, s.x), p.inv_len, s.x * p.inv_len);
+            means[1] = s.y * p.inv_len;
         }
 #pragma unroll
         for (int q = 0; q < R; ++q) {
@@ -782,8 +785,8 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_backward_kernel(
                     cols.load(ring + (stage * R + q) * 2 * pitch + cols.offset(at), fx);
                     cols.load(ring + ((stage * R + q) * 2 + 1) * pitch + cols.offset(at), fd);
                 }
-                const float rq = r[q], b0 = p.mean ? -rq * (sums[2 * q] * inv_k) : 0.f;
-                const float a0 = -rq * (rq * (sums[2 * q + 1] * inv_k));   // -r·c2, c2 = r·mean(u·d)
+                const float rq = r[q], b0 = p.mean ? -rq * means[2 * q] : 0.f;
+                const float a0 = -rq * (rq * means[2 * q + 1]);   // -r·c2, c2 = r·mean(u·d)
                 const Pair c = pair(-mu[q], -mu[q]), rr = pair(rq, rq), pa = pair(a0, a0), pb = pair(b0, b0);
 #pragma unroll
                 for (int e = 0; e < H; ++e) {

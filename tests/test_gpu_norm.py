@@ -305,3 +305,18 @@ def test_rows_of_one_value_have_no_deviation(T, K, xt):
     if K % 128 == 0:
         q, sfa = ops.layer_norm_cast(cuda(x))
         assert not q.any() and (sfa[:, :T] == 1).all()
+
+
+@pytest.mark.parametrize("K", [200, 768, 1000, 1001, 7168, 8191, 12288, 20001])
+@pytest.mark.parametrize("T", [4, 300])
+@pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
+def test_equal_gradients_of_equal_values_cancel(T, K, xt):
+    """dy of one value in a row of one value: u is its own mean and xh is 0, so dx is 0 and not r times an ulp of u.
+    The values have 8 bits at most and K < 2^15, so every sum of them is exact in fp32."""
+    x = torch.tensor([3.0, 1000.0, -49920.0, 0.375]).repeat(T // 4)
+    dy = torch.tensor([1.0, 3.0, -125.0, 0.375]).repeat(T // 4)
+    rstd = torch.full((T,), 316.0)
+    rows = [v[:, None].expand(T, K).to(xt).contiguous() for v in (dy, x)]
+    dx, _, db = ops.layer_norm_backward(cuda(rows[0]), cuda(rows[1]), None, cuda(x), cuda(rstd))
+    assert not dx.any()
+    assert torch.equal(db.cpu(), dy.sum().expand(K))
