@@ -505,10 +505,11 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
         }
         if (__any_sync(0xFFFFFFFFu, again)) {
             // all values that may belong to the k largest, then their order by the 64-bit values
-            const float last = __shfl_sync(0xFFFFFFFFu, v - tol, k - 1);
+            // (next to the lowest value, v - tol would be -inf, which every empty place reaches)
+            const float last = fmaxf(__shfl_sync(0xFFFFFFFFu, v - tol, k - 1), -CUDART_MAX_NORMAL_F);
             int n = k + 1;
             for (; n < 32 && redux_max(c[0]) >= last; ++n) take(n);
-            if (redux_max(c[0]) >= last && last > -CUDART_INF_F) return true;   // still more of them
+            if (redux_max(c[0]) >= last) return true;   // still more of them
             id = expert();
             xs = id >= 0 ? fminf(static_cast<float>(row[id]), CUDART_MAX_NORMAL_F) : 0.f;
             const double sum64 = softmax && !by_logit ? route_sum_f64(p, row, mx) : 1.0;

@@ -308,3 +308,24 @@ def test_gaps_of_every_size(score, E, groups, topk_groups, top):
     b2[3] = FMAX
     check(x[12:], b2, 8, score=score)
     assert _lib.dg_get_device_error() == _lib.DG_OK
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [64, 100, 1024])
+def test_many_values_next_to_the_lowest(score, E):
+    """More values at and one step above the type's lowest than a warp's lanes hold: their order is that of the
+    values, in the logits and in the biases."""
+    up = float(np.nextafter(np.float32(-FMAX), np.float32(0)))
+    x = torch.full((4, E), -FMAX)
+    x[0, E // 2:] = up
+    x[1, 1::2] = up
+    x[2, 5:] = up
+    x[2, 40:43] = 0.5
+    x[3, E - 3:] = up
+    for k in (1, 8, 30):
+        check(x, None, k, score=score)
+        check(x[:, :E // 4 * 4].contiguous(), None, k, 4, 2, 1, score)
+    y, _ = logits(5, E, torch.float32, seed=21)
+    for row in x:
+        check(y, row, 8, score=score)
+    assert _lib.dg_get_device_error() == _lib.DG_OK
