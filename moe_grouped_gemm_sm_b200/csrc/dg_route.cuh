@@ -399,7 +399,9 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
             a1 = softmax ? ex2_approx(1.44269504f * (a1 - mx)) : sigmoid_approx(a1);
             if (a2 > -CUDART_INF_F) a2 = softmax ? ex2_approx(1.44269504f * (a2 - mx)) : sigmoid_approx(a2);
         }
-        const float mine = p.group_top == 2 && a2 > -CUDART_INF_F ? a1 + a2 : a1;
+        // Two values are taken by halves: their sum may not fit fp32, and -inf stands for a group without experts.
+        const float part = p.group_top == 2 ? 0.5f : 1.f;
+        const float mine = p.group_top == 2 && a2 > -CUDART_INF_F ? part * a1 + part * a2 : part * a1;
         int rank = 0;
         if (p.groups == 8) {
             // among lanes 0 .. 7 (the others rank among themselves and are not asked)
@@ -422,7 +424,7 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
             const float in = -redux_max(keep ? -mine : -CUDART_INF_F);
             const float out = redux_max(keep ? -CUDART_INF_F : mine);
             const float unit = by_logit ? (softmax ? 0x1p-17f : 0x1p-20f) : tol_score;
-            const float tol = 2.f * unit + 0x1p-21f * (fabsf(in) + fabsf(out));
+            const float tol = part * (2.f * unit) + 0x1p-21f * (fabsf(in) + fabsf(out));
             if (out > -CUDART_INF_F && !(in - out > tol)) {
                 const bool open = lane < p.groups && !(keep ? mine - out > tol : in - mine > tol);
                 const uint32_t compete = __ballot_sync(0xFFFFFFFFu, open);

@@ -329,3 +329,18 @@ def test_many_values_next_to_the_lowest(score, E):
     for row in x:
         check(y, row, 8, score=score)
     assert _lib.dg_get_device_error() == _lib.DG_OK
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_group_values_beyond_fp32(score):
+    """Two choice values of a group may sum to more than fp32 holds, on either side: the groups keep their order, and
+    a group of very low values is not one of no experts."""
+    x, _ = logits(40, 32, torch.float32, seed=22)
+    for low in ([-3e38, -2e38, -2.5e38, -3.2e38], [3e38, 3.3e38, 2e38, 2.5e38], [-3e38, -3.3e38, 3e38, 1.0],
+                [-3.3e38, -3e38, -float("inf"), -float("inf")], [FMAX, -FMAX, FMAX, -FMAX]):
+        b = torch.tensor(low).repeat_interleave(8)
+        for kept in (1, 2, 3):
+            check(x, b, 4, 4, kept, 2, score)
+        check(x, b, 8, 8, 3, 2, score)
+        check(x.repeat(1, 8), b.repeat(8), 8, 8, 3, 2, score)
+    assert _lib.dg_get_device_error() == _lib.DG_OK
