@@ -419,14 +419,17 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
         const bool keep = lane < p.groups && rank < p.topk_groups;
         uint32_t kept = __ballot_sync(0xFFFFFFFFu, keep);
         if (sums) {
-            // is the border between the groups wide enough? Groups too close to it compete again by
-            // their 64-bit values; the others are truly above or below all of those.
-            const float in = -redux_max(keep ? -mine : -CUDART_INF_F);
-            const float out = redux_max(keep ? -CUDART_INF_F : mine);
+            // Is the border between the groups wide enough? A group's value may be off by its scores' errors and by the
+            // roundings of what was added: of both choice values, which a bias can make far larger than their sum.
+            // Groups that reach across the border compete again by their 64-bit values; the others are truly above or
+            // below all of those.
             const float unit = by_logit ? (softmax ? 0x1p-17f : 0x1p-20f) : tol_score;
-            const float tol = part * (2.f * unit) + 0x1p-21f * (fabsf(in) + fabsf(out));
-            if (out > -CUDART_INF_F && !(in - out > tol)) {
-                const bool open = lane < p.groups && !(keep ? mine - out > tol : in - mine > tol);
+            const float size = fabsf(part * a1) + (p.group_top == 2 && a2 > -CUDART_INF_F ? fabsf(part * a2) : 0.f);
+            const float off = a1 > -CUDART_INF_F ? 0.5f * unit + 0x1p-22f * size : 0.f;
+            const float in = -redux_max(keep ? off - mine : -CUDART_INF_F);   // the lowest kept group at its lowest
+            const float out = redux_max(keep ? -CUDART_INF_F : mine + off);   // the highest of the others at its highest
+            if (out > -CUDART_INF_F && !(in > out)) {
+                const bool open = lane < p.groups && !(keep ? mine - off > out : in > mine + off);
                 const uint32_t compete = __ballot_sync(0xFFFFFFFFu, open);
                 const double sum64 = softmax && !by_logit ? route_sum_f64(p, row, mx) : 1.0;
                 double exact = -CUDART_INF;

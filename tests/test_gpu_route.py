@@ -344,3 +344,28 @@ def test_group_values_beyond_fp32(score):
         check(x, b, 8, 8, 3, 2, score)
         check(x.repeat(1, 8), b.repeat(8), 8, 8, 3, 2, score)
     assert _lib.dg_get_device_error() == _lib.DG_OK
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size,spread", [(1000.0, 1e-2), (1000.0, 1e-3), (3e4, 0.1), (1e5, 1.0)])
+def test_group_values_that_cancel(score, size, spread):
+    """Biases of both signs in a group: each choice value is rounded at the bias's size, while the group's value is
+    of the scores' size. The choice is that of the 64-bit values, which hold the scores to 2^-53 of the bias."""
+    T, E, G = 20000, 64, 8
+    g = torch.Generator().manual_seed(int(size))
+    x = 0.3 + spread * torch.randn(T, E, generator=g)
+    b = torch.full((E,), -size)
+    b[::E // G] = size
+    c = (torch.softmax(x.double(), 1) if score == "softmax" else torch.sigmoid(x.double())) + b.double()
+    best = c.view(T, G, -1).topk(2, dim=2).values.sum(2)
+    # rows whose groups or experts 64 bits cannot tell apart are left out: 4 roundings of the bias between them
+    gap = best.sort(1).values.diff(dim=1).amin(1)
+    kept = best.topk(4, dim=1).indices
+    on = torch.zeros(T, G, dtype=torch.bool).scatter_(1, kept, True).repeat_interleave(E // G, 1)
+    top = c.masked_fill(~on, -float("inf")).topk(7, dim=1)
+    gap = torch.minimum(gap, -top.values.diff(dim=1).amax(1))
+    sure = gap > 8 * 2.0 ** -53 * size
+    assert sure.float().mean() > 0.98
+    for rows in (slice(0, T), slice(0, 60)):
+        _, ids = ops.moe_route(x[rows].cuda(), 6, bias=b.cuda(), groups=G, topk_groups=4, group_top=2, score=score)
+        assert torch.equal(ids.cpu().long()[sure[rows]], top.indices[rows, :6][sure[rows]])
