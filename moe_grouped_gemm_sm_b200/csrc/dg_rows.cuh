@@ -40,7 +40,8 @@ __device__ __forceinline__ int ld_shared_cluster(uint32_t addr) {
 }
 
 // Shared memory: s_first[G] (first row of the expert), s_total[G] (its pairs), s_count[G] (those of this block, read
-// by the others), s_next[warps][G] (a warp's pairs, then its next row of the expert).
+// by the others), s_next[warps][G] (a warp's pairs, then its next row of the expert; masked its next place among the
+// expert's rows, since g·M plus the pairs of an expert that has too many may pass 2^31).
 template <bool MASKED, int BITS>
 __global__ void __launch_bounds__(32 * LAYOUT_MAX_WARPS) layout_kernel(const __grid_constant__ LayoutParams p) {
     extern __shared__ int s_layout[];
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(32 * LAYOUT_MAX_WARPS) layout_kernel(const __g
         if (g < G) {
             if (MASKED && rank == 0 && p.counts) p.counts[g] = min(total, p.M);
             s_first[g] = first;
-            int next = first + before;
+            int next = MASKED ? before : first + before;
             for (int w = 0; w < warps; ++w) {
                 const int count = s_next[w * G + g];
                 s_next[w * G + g] = next;
@@ -138,9 +139,11 @@ __global__ void __launch_bounds__(32 * LAYOUT_MAX_WARPS) layout_kernel(const __g
         int row = -1;
         if (in) {
             row = s_next[warp * G + e] + __popc(same & ((1u << lane) - 1u));
-            if (row >= (MASKED ? s_first[e] + p.M : p.M)) {
+            if (row >= p.M) {
                 row = -1;
                 lost = true;
+            } else if (MASKED) {
+                row += s_first[e];
             }
         }
         __syncwarp();

@@ -467,3 +467,17 @@ def test_refusals():
                  lambda: ops.moe_combine(x[:, :12].contiguous(), ids), lambda: ops.moe_combine(x, ids[:, :0].contiguous())):
         with pytest.raises((_lib.DgError, RuntimeError)):
             call()
+
+
+def test_masked_rows_next_to_2_to_31():
+    """The last expert of 1024 with more pairs than M_max = 2^21 - 1: the pairs beyond it get -1, although the rows they
+    would have pass 2^31."""
+    G, M, n = 1024, 2 ** 21 - 1, 2 ** 21 + 5000
+    ids = torch.full((n // 8, 8), G - 1, dtype=torch.int32, device="cuda")
+    ids[0] = 0
+    dst, mm = ops.moe_layout_masked(ids, G, M)
+    place = torch.arange(n - 8, device="cuda")
+    ref = torch.cat([torch.arange(8, device="cuda"), torch.where(place < M, (G - 1) * M + place, -1)])
+    assert torch.equal(dst.reshape(-1).long(), ref)
+    assert mm.tolist() == [8] + [0] * (G - 2) + [M]
+    assert _lib.dg_get_device_error() == _lib.DG_ERR_DEVICE
