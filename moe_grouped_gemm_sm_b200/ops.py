@@ -10,7 +10,8 @@ Each function checks that its tensors are contiguous CUDA tensors, allocates wha
 
 The operators around the experts' products (``layer_norm*``, ``moe_*``, ``cast_per_token_scatter_topk``) also
 check types and shapes and that all tensors are on one device; they run on that device, and
-allocate their results and workspaces for the stream that they run on. The gradients are
+allocate their results and workspaces for the stream that they run on. Tensors start on 16 bytes; the
+routing, its gradient and the layouts also take slices that do not, and copy them first. The gradients are
 explicit functions; no autograd graph is built.
 """
 from __future__ import annotations
@@ -222,6 +223,17 @@ def _check_2d(name, t, dtype, device=None):
     return s
 
 
+def _any_start(entry, *args):
+    """entry(*args), and where the C ABI refuses an input that does not start on 16 bytes (a slice of a batch; the refusal
+    comes before anything is queued) the same with copies of such inputs. Asking each tensor first costs 0.4 us a call."""
+    try:
+        entry(*args)
+    except _lib.DgError as e:
+        if e.status != _lib.DG_ERR_ALIGNMENT:
+            raise
+        entry(*(a.clone() if isinstance(a, torch.Tensor) and a.data_ptr() % 16 else a for a in args))
+
+
 def _check_sizes(*sizes):
     """The C ABI takes 32-bit sizes; ctypes would cut larger ones off without a word."""
     if max(sizes) >= 2 ** 31 or min(sizes) < -2 ** 31:
@@ -355,8 +367,8 @@ def moe_route(logits, k, bias=None, groups=1, topk_groups=1, group_top=1, score=
     ids = logits.new_empty((T, k), dtype=torch.int32)
     weights = torch.empty_like(ids, dtype=torch.float32)
     if T:
-        _lib.dg_moe_route(logits, bias, ids, weights, T, E, k, groups, topk_groups, group_top, s, int(renorm), scale,
-                          _TYPES[logits.dtype], _raw_stream(dev))
+        _any_start(_lib.dg_moe_route, logits, bias, ids, weights, T, E, k, groups, topk_groups, group_top, s, int(renorm),
+                   scale, _TYPES[logits.dtype], _raw_stream(dev))
     return weights, ids
 
 
@@ -373,8 +385,8 @@ def moe_route_backward(grad_weights, logits, ids, score="softmax", renorm=True, 
             return moe_route_backward(grad_weights, logits, ids, score, renorm, scale)
     g = torch.empty_like(logits)
     if T:
-        _lib.dg_moe_route_backward(grad_weights, logits, ids, g, T, E, k, s, int(renorm), scale, _TYPES[logits.dtype],
-                                   _raw_stream(dev))
+        _any_start(_lib.dg_moe_route_backward, grad_weights, logits, ids, g, T, E, k, s, int(renorm), scale,
+                   _TYPES[logits.dtype], _raw_stream(dev))
     return g
 
 
@@ -393,7 +405,7 @@ def moe_layout_contiguous(ids, G, M_sum=None, stream=None):
     dst = torch.empty_like(ids)
     layout = ids.new_empty(M_sum)
     ks = ids.new_empty(G)
-    _lib.dg_moe_layout_contiguous(ids, dst, layout, ks, T, k, G, M_sum, _raw_stream(dev))
+    _any_start(_lib.dg_moe_layout_contiguous, ids, dst, layout, ks, T, k, G, M_sum, _raw_stream(dev))
     return dst, layout, ks
 
 
@@ -408,7 +420,7 @@ def moe_layout_masked(ids, G, M_max, stream=None):
             return moe_layout_masked(ids, G, M_max)
     dst = torch.empty_like(ids)
     masked_m = ids.new_empty(G)
-    _lib.dg_moe_layout_masked(ids, dst, masked_m, T, k, G, M_max, _raw_stream(dev))
+    _any_start(_lib.dg_moe_layout_masked, ids, dst, masked_m, T, k, G, M_max, _raw_stream(dev))
     return dst, masked_m
 
 

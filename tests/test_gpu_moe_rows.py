@@ -481,3 +481,44 @@ def test_masked_rows_next_to_2_to_31():
     assert torch.equal(dst.reshape(-1).long(), ref)
     assert mm.tolist() == [8] + [0] * (G - 2) + [M]
     assert _lib.dg_get_device_error() == _lib.DG_ERR_DEVICE
+
+
+def shifted(t, by=1):
+    """The same values in memory that does not start on a 16-byte boundary."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device=t.device)
+    s = buf[by:].view(t.shape)
+    s.copy_(t)
+    assert s.data_ptr() % 16 and s.is_contiguous()
+    return s
+
+
+@pytest.mark.parametrize("stream", [False, True])
+def test_slices_of_a_batch(stream):
+    """ids, logits, biases and gradients of the routing and the layouts may start anywhere in a tensor: a slice of a batch
+    gives what a copy of it gives."""
+    T, E, k = 37, 48, 3
+    g = torch.Generator().manual_seed(13)
+    gw, bias = torch.randn(T, k, generator=g).cuda(), (0.1 * torch.randn(E, generator=g)).cuda()
+    st = torch.cuda.Stream() if stream else None
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.randn(T, E, generator=g).to(dtype).cuda()
+        w, ids = ops.moe_route(x, k, bias=bias, groups=6, topk_groups=3)
+        ref = [w, ids, ops.moe_route_backward(gw, x, ids), *ops.moe_layout_contiguous(ids, E), *ops.moe_layout_masked(ids, E, T)]
+        torch.cuda.synchronize()
+        xs, bs, gs, si = shifted(x), shifted(bias), shifted(gw), shifted(ids)
+        torch.cuda.synchronize()
+        got = [*ops.moe_route(xs, k, bias=bs, groups=6, topk_groups=3, stream=st), ops.moe_route_backward(gs, xs, si, stream=st),
+               *ops.moe_layout_contiguous(si, E, stream=st), *ops.moe_layout_masked(si, E, T, stream=st)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, ref))
+        assert torch.equal(ops.moe_route_backward(gw, x, si), ref[2])
+    assert torch.equal(ops.moe_layout_masked(ids[1:], E, T)[1], ops.moe_layout_masked(ids[1:].clone(), E, T)[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [*ops.moe_layout_contiguous(si, E), ops.moe_route_backward(gs, xs, si)]
+    si.fill_(-1)
+    si.copy_(ids)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, [*ref[3:6], ref[2]]))
+    assert _lib.dg_get_device_error() == _lib.DG_OK
