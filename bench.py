@@ -324,12 +324,15 @@ def _json_default(o):
 
 
 def source_digest():
-    """sha1 of the CUDA sources: the DRAM traffic stored under profiles/ holds for this digest."""
+    """sha1 of the GEMMs' CUDA sources: the kernels, what they include, and the file that plans and launches them (the
+    casts and the operators around the products have files of their own). The DRAM traffic of the GEMMs stored under
+    profiles/ holds for this digest."""
     import glob
     import hashlib
     h = hashlib.sha1()
     csrc = os.path.join(ROOT, "moe_grouped_gemm_sm_b200", "csrc")
-    for f in sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh"))):
+    for f in sorted([os.path.join(csrc, n) for n in ("dg_api.cu", "dg_ptx.cuh")] +
+                    glob.glob(os.path.join(csrc, "dg_gemm*.cuh"))):
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode() + b"\0" + fh.read())
     return h.hexdigest()

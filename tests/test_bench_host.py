@@ -78,3 +78,27 @@ def test_k_grouped_problem_sizes_and_bytes():
     assert p["K"] == T and p["x"].shape == (T, 256) and p["w"].shape == (T, 128)
     assert p["flops"] == 2.0 * 256 * 128 * T
     assert bench.algorithmic_bytes(p) == T * 256 + T * 128 + 4 * (T // 128) * (256 + 128) + 4 * 8 * 256 * 128
+
+
+def test_source_digest_follows_the_gemm_sources(tmp_path, monkeypatch):
+    """The digest changes with every file that a GEMM is built from, and with no other."""
+    import os
+    import shutil
+    real = os.path.join(bench.ROOT, "moe_grouped_gemm_sm_b200", "csrc")
+    csrc = tmp_path / "moe_grouped_gemm_sm_b200" / "csrc"
+    shutil.copytree(real, csrc)
+    before = bench.source_digest()
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    assert bench.source_digest() == before
+    for name in sorted(os.listdir(csrc)):
+        text = (csrc / name).read_bytes()
+        (csrc / name).write_bytes(text + b"// another line\n")
+        gemm = name in ("dg_api.cu", "dg_ptx.cuh") or name.startswith("dg_gemm")
+        assert (bench.source_digest() != before) == gemm, name
+        (csrc / name).write_bytes(text)
+    # a GEMM file includes none but the ones counted
+    for name in os.listdir(csrc):
+        if name.startswith("dg_gemm") or name == "dg_ptx.cuh":
+            for line in (csrc / name).read_text().splitlines():
+                if line.startswith('#include "'):
+                    assert line.split('"')[1].startswith(("dg_gemm", "dg_ptx")), (name, line)
