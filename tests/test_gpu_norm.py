@@ -320,3 +320,26 @@ def test_equal_gradients_of_equal_values_cancel(T, K, xt):
     dx, _, db = ops.layer_norm_backward(cuda(rows[0]), cuda(rows[1]), None, cuda(x), cuda(rstd))
     assert not dx.any()
     assert torch.equal(db.cpu(), dy.sum().expand(K))
+
+
+def test_two_graphs_share_the_backward_workspace():
+    """Two graphs captured on one memory pool: the backward pass's workspace of the first is free again when the second is
+    captured, so both may use the same memory. Replayed in any order, each gives the eager bits."""
+    x, w, b = (t.cuda() for t in make(700, 1536, torch.bfloat16, torch.float32, False, seed=14))
+    dys = [torch.randn(700, 1536, generator=torch.Generator().manual_seed(s)).bfloat16().cuda() for s in (1, 2)]
+    _, mean, rstd = ops.layer_norm(x, w, b, stats=True)
+    refs = [ops.layer_norm_backward(dy, x, w, mean, rstd) for dy in dys]
+    torch.cuda.synchronize()
+    pool, graphs = None, []
+    for dy in dys:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=pool):
+            out = ops.layer_norm_backward(dy, x, w, mean, rstd)
+        pool = graph.pool()
+        graphs.append((graph, out))
+    for i in (0, 1, 1, 0, 0, 1):
+        for o in graphs[i][1]:
+            o.zero_()
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(graphs[i][1], refs[i]))
