@@ -403,18 +403,9 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
         const float part = p.group_top == 2 ? 0.5f : 1.f;
         const float mine = p.group_top == 2 && a2 > -CUDART_INF_F ? part * a1 + part * a2 : part * a1;
         int rank = 0;
-        if (p.groups == 8) {
-            // among lanes 0 .. 7 (the others rank among themselves and are not asked)
-#pragma unroll
-            for (int h = 1; h < 8; ++h) {
-                const float v = __shfl_xor_sync(0xFFFFFFFFu, mine, h);
-                rank += ((lane ^ h) < lane ? v >= mine : v > mine) ? 1 : 0;
-            }
-        } else {
-            for (int h = 0; h < p.groups; ++h) {
-                const float v = __shfl_sync(0xFFFFFFFFu, mine, h);
-                rank += (v > mine || (v == mine && h < lane)) ? 1 : 0;
-            }
+        for (int h = 0; h < p.groups; ++h) {
+            const float v = __shfl_sync(0xFFFFFFFFu, mine, h);
+            rank += (v > mine || (v == mine && h < lane)) ? 1 : 0;
         }
         const bool keep = lane < p.groups && rank < p.topk_groups;
         uint32_t kept = __ballot_sync(0xFFFFFFFFu, keep);
