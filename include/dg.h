@@ -300,8 +300,9 @@ DG_API long long dg_layer_norm_backward_workspace(int T, int K);
  *   (1 or 2) largest c, and the topk_groups groups of largest value are kept;
  *   ids = the k experts of largest c in the kept groups, in falling order of c;
  *   w_j = s[ids_j], divided by their sum if renorm, times scale. The bias is in no weight.
- * Equal values are taken in the order of their index. The choice follows the real values: scores
- * that differ by less than an fp32 rounding are not confused. A logit of -inf or a bias of -inf
+ * Equal values are taken in the order of their index. The choice is that of the 64-bit values: scores
+ * that differ by less than an fp32 rounding are not confused (without a bias the logits are compared, which holds where
+ * 64-bit scores are equal, too). A logit of -inf or a bias of -inf
  * takes the expert out of the choice; so does a NaN, which also sets the device error word; a
  * logit of +inf counts as the largest finite fp32. Where fewer than k experts are left, the last
  * ids are -1 and their weights 0. A group with fewer than group_top experts left counts those

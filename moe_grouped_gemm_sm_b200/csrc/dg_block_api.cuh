@@ -9,7 +9,8 @@ namespace {
 
 constexpr int kNormMaxK = 32768;
 constexpr int kNormLongParts = 64;    // row parts of the dw / db sums of long rows
-constexpr int kNormSms = 148;         // the SMs that the norm's backward pass is cut for
+constexpr int kNormSms = 148;         // the SMs that rings are cut for, not those of the current device: the backward
+                                      // pass's workspace is asked for before there need be one
 constexpr int kNormRing = 200 << 10;  // bytes of shared memory for the ring of rows
 
 constexpr int kMaxRows = 1 << 30;

@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) layer_norm_kernel(const Norm
                 s2 += f[j][e] * f[j][e];
             }
         }
-    const float r = rsqrtf(row_sum(s2, s_red[1]) / static_cast<float>(K) + p.eps);   // within 2 ulp
+    // within 2 ulp, where a root and a quotient would be within 1; the sum of K squares weighs more
+    const float r = rsqrtf(row_sum(s2, s_red[1]) / static_cast<float>(K) + p.eps);
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mu;
         if (p.rstd) p.rstd[row] = r;
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) layer_norm_kernel(const Norm
 // COLS_VECTORS: K is a whole number of 16-byte vectors; a thread owns vectors of V columns, copies and reads its own
 // only, and the ring needs no barrier. COLS_EXACT: and K = N·blockDim.x, so that nothing needs a bounds check (the
 // checks' zero registers and branches were a quarter of the backward pass's instructions). COLS_SINGLE: rows begin
-// anywhere: a stage takes the 16-byte chunks that hold its row (the bytes behind the tensor's end as zeros), a thread
+// anywhere in the tensor (which starts on 16 bytes): a stage takes the 16-byte chunks that hold its row (the bytes behind the tensor's end as zeros), a thread
 // owns single columns blockDim.x apart, and a barrier stands between the copies and the reads.
 enum : int { COLS_SINGLE = 0, COLS_VECTORS = 1, COLS_EXACT = 2 };
 constexpr int NORM_STAGES = 3, NORM_RING_THREADS = 512;   // 512 threads an SM leave 128 registers each
@@ -408,8 +409,9 @@ __device__ __forceinline__ void ring_step(F refill) {
 // barrier. (Both means are sums divided by their count to the last place, so a row of equal values has deviation 0, as
 // in the kernel above. The rounding of the warp's mean enters the mean square squared, and times its distance from the
 // row's mean.)
-// 8192 x 7168 bf16: 50 us, 72 % of the copy rate (a block a row, the kernel above: 62); fp32 80 us, 90 %. What is left
-// in bf16 is instructions: 14 warps an SM, which the registers allow, issue in half of the cycles.
+// 8192 x 7168 bf16: 49.5 us, 73 % of the copy rate (a block a row, the kernel above: 62), RMS 41 us, 87 %; fp32 81 us,
+// 88 %. What is left in bf16 is latency at few warps: 14 warps an SM issue in half of the cycles. (8 columns a thread,
+// twice the warps, are there for rows of up to 256; on long rows they were tried in the backward pass only.)
 template <typename XT, typename WT, int N, int R, int COLS>
 __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_ring_kernel(const __grid_constant__ NormParams p) {
     using Cols = NormColumns<XT, N, COLS>;
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(NORM_RING_THREADS) layer_norm_ring_kernel(cons
         for (int q = 0; q < R; ++q) {
             const int t = row + q * step;
             if (t >= p.T) break;   // the same for the whole team
-            const float r = rsqrtf(fmaf(m2[q], inv_k, p.eps));   // within 2 ulp
+            const float r = rsqrtf(fmaf(m2[q], inv_k, p.eps));   // within 2 ulp, as in the kernel above
             if (tid == 0) {
                 if (p.mean) p.mean[t] = mu[q];
                 if (p.rstd) p.rstd[t] = r;
@@ -644,7 +646,8 @@ __global__ void __launch_bounds__(256) layer_norm_dwdb_kernel(const NormBackPara
 
 // dx, and the sums of dw and db, in one pass over dy and x: HBM-bound (three tensors of T·K). Teams, columns
 // and the ring are those of the forward kernel, with rows of x and dy side by side; a thread's columns' dw
-// and db stay in registers to the end, and R rows cost one barrier for their sums of u and u·(x - mu).
+// and db stay in registers to the end (one running fp32 sum over the rows of a team: 56 of 8192), and R rows cost one
+// barrier for their sums of u and u·(x - mu).
 // dx = (dy·r)·w - r·c1 - xh·(r·c2) with c1 = mean(u), c2 = r·mean(u·(x - mu)). c1 is divided to the last place: where
 // all u of a row are equal it has to cancel them, and an ulp left over would be multiplied by r.
 // The teams' sums meet in shared memory and go to part[blockIdx.x] in a fixed order.

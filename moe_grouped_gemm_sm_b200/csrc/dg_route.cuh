@@ -22,7 +22,7 @@ namespace dg {
 
 enum : int { SCORE_SOFTMAX = 0, SCORE_SIGMOID = 1 };
 constexpr int ROUTE_WARPS = 4;    // tokens per block
-constexpr int ROUTE_BLOCKS = 7;   // blocks per SM (for up to 256 experts)
+constexpr int ROUTE_BLOCKS = 7;   // blocks per SM (for up to 256 experts; measured with 256, below)
 constexpr int ROUTE_MAX_E = 1024, ROUTE_MAX_K = 32, ROUTE_MAX_GROUPS = 32;
 
 struct RouteParams {
@@ -257,10 +257,13 @@ __device__ __forceinline__ void sort_falling(float (&v)[N]) {
 // chosen wrongly: then all that may belong to the k largest, one in a lane, are put in the order of
 // their 64-bit values, and groups at the border likewise. Neighbours with the same logit and the
 // same bias are equal in truth and need no second look. With N(0,1.5) logits over 256 experts that
-// is about 40 of 16384 tokens.
+// is about 40 of 16384 tokens. (The softmax sum of the hardware's exponentials also divides the weights that are not
+// renormalised: 2^-22 of each term and 2^-24 of its distance from the largest.)
 // Bound by instructions (some 880 a token and warp with 8 groups over 256 experts): 16384 tokens take 21 us, 65536
-// 71 us; every value in 64 bits took 122 us for 16384. Traffic alone would be 2.7 us. 7 blocks an SM (72 registers)
-// against 8, 6 and 5: 71, 74, 72 and 76 us for 65536 tokens.
+// 71 us; every value in 64 bits took 122 us for 16384. Traffic alone would be 2.7 us. 7 blocks an SM (72 registers,
+// 92 bytes of spills; 40, 20 and 4 for 128, 64 and 32 experts, where other counts were not timed) against 8, 6 and 5:
+// 71, 74, 72 and 76 us for 65536 tokens. The ranking of the groups by one loop for any number of them, against one of its
+// own for 8: 70.6 and 72.7 us.
 template <typename LT, int EPL>
 __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&b)[EPL], int t, int lane) {
     const bool softmax = p.score == SCORE_SOFTMAX, by_logit = p.bias == nullptr;
@@ -487,7 +490,7 @@ __device__ __forceinline__ bool route_token(const RouteParams &p, const float (&
     };
     int id = expert(), place = lane;
     float xs = id >= 0 ? fminf(static_cast<float>(row[id]), CUDART_MAX_NORMAL_F) : 0.f;
-    if (!(sizeof(LT) == 2 && by_logit && EPL <= 32)) {   // bf16 logits have the bits to spare: their order is exact
+    if (!(sizeof(LT) == 2 && by_logit)) {   // bf16 logits have the 5 bits to spare: their order is exact
         const float bs = id >= 0 && !by_logit ? p.bias[id] : 0.f;
         const float v1 = __shfl_down_sync(0xFFFFFFFFu, v, 1), x1 = __shfl_down_sync(0xFFFFFFFFu, xs, 1);
         const float b1 = __shfl_down_sync(0xFFFFFFFFu, bs, 1);

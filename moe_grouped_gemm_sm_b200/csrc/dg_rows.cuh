@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 6) combine_backward_kernel(co
             }
         }
         if (p.gw) {
-            if (j0) __syncthreads();   // the last 8 rows' sums have been read
+            if (j0) __syncthreads();   // the last BACK_ROWS rows' sums have been read
 #pragma unroll
             for (int q = 0; q < BACK_ROWS; ++q) {
                 const float s = warp_sum(dot[q]);
