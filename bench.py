@@ -14,9 +14,11 @@ synthetic recipe of moe_grouped_gemm_sm_b200.synth: A, B ~ N(0,1) and C ~ N(0,0.
 contiguous experts hold U{2048..6144} rows padded to 128; masked experts U{64..256} rows.
 
 The default workload (the one the headline number is quoted on) is the dense prefill set:
-M = 4096 with (N,K) in the six DeepSeek-V3 GEMM shapes and a C addend. The same JSON line then
-carries a "workloads" object with the other page configurations, each timed in its own region
-with its own roofline and per-problem times: the 64x2112x7168 decode shape with C = 0
+M = 4096 with (N,K) in the six DeepSeek-V3 GEMM shapes and a C addend. The same JSON line (the only
+one on standard output, a few kilobytes) then carries a "workloads" object with the other page
+configurations, each timed in its own region: its value, time and roofline fraction. The full record, with
+every workload's roofline and per-problem times, goes to standard error as one JSON line
+{"detail": ...}. The configurations: the 64x2112x7168 decode shape with C = 0
 (config1), the M = 64 and M = 128 decode sets with the L2 flushed before every step (cold) and
 back to back (warm), the G = 8 contiguous and the G = 16 masked MoE sets.
 
@@ -349,6 +351,19 @@ def stored_traffic(workload):
     if not isinstance(entry, dict) or entry.get("source_sha1") != source_digest():
         return None
     return entry.get("bytes_per_launch")
+
+
+def result_line(result):
+    """The line for standard output: the full record without the per-problem times, and of each of the other
+    workloads its value, time per step and roofline fraction. Callers that keep the last few kilobytes of the output
+    get it whole (the full record is some 25 KB)."""
+    out = {k: v for k, v in result.items() if k not in ("per_problem", "workloads")}
+    if "roofline" in out:
+        out["roofline"] = {k: v for k, v in out["roofline"].items() if k not in ("timing", "frac_of_burst_peak",
+                                                                                 "frac_of_sustained_peak")}
+    if "workloads" in result:
+        out["workloads"] = {k: {"value": w["value"], "ms": w["ms_per_step"], "frac": w["roofline"]["frac"]} for k, w in result["workloads"].items()}
+    return out
 
 
 class CudaArm:
@@ -772,7 +787,8 @@ def run_cuda(args):
         result["workloads"] = subs
 
     if rank == 0:
-        print(json.dumps(result, default=_json_default), flush=True)
+        print(json.dumps({"detail": result}, default=_json_default), file=sys.stderr, flush=True)
+        print(json.dumps(result_line(result), default=_json_default), flush=True)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()

@@ -102,3 +102,40 @@ def test_source_digest_follows_the_gemm_sources(tmp_path, monkeypatch):
             for line in (csrc / name).read_text().splitlines():
                 if line.startswith('#include "'):
                     assert line.split('"')[1].startswith(("dg_gemm", "dg_ptx")), (name, line)
+
+
+def test_result_line_is_short_and_whole():
+    """The line on standard output fits the 2.8 KB that a caller keeps of it, with every key of the contract and every
+    other workload's value."""
+    import json
+    problem = {"N": 24576, "K": 16384, "rows": 4096, "G": 1, "layout": "nt", "flops": 309237645312.0, "gemm_us": 1351.18,
+               "kernel": "gemm_kernel (CTA pairs, last-wave split 7)", "tflops": 1765.5, "roof_frac": 0.541}
+    roof = {"bound": "tensor", "achieved": 1820.8, "peak": 3262.0, "unit": "TFLOP/s", "frac": 0.5582,
+            "peak_source": "measured: 2 x bf16_tflops_sustained (the power cap was active or the clock below max); "
+                           "fp8 = 2x bf16 nominal ratio", "frac_of_burst_peak": 0.5582, "frac_of_sustained_peak": 0.6543,
+            "roofline_time_frac": 0.5994, "timing": "t" * 250, "traffic": 311666176.0,
+            "kernel": "gemm_kernel (CTA pairs) + gemm_kernel (CTA pairs, last-wave split 7) (6 problems, aggregate over "
+                      "launches)"}
+    wl = bench.WORKLOADS["prefill"]
+    result = {"metric": bench.METRIC, "value": 1635.82, "unit": "TFLOP/s", "n_gpus": 1, "steps": 200, "warmup": 10,
+              "ms_per_step": 1.1576, "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "e4m3",
+              "data": "synthetic",
+              "config": {"workload": wl["desc"], "shapes_NK": [list(s) for s in wl["shapes"]], "parallelism": "single GPU",
+                         "step": "per-token cast of A + GEMM per problem; weights cast offline",
+                         "l2": max(bench.L2_TEXT.values(), key=len)},
+              "roofline": roof, "per_problem": [problem] * 6, "weight_cast": {"gbs": 1650.7, "ms_total": 0.42},
+              "e2e": {"value": 65.06, "unit": "TFLOP/s", "h2d_bytes_per_step": 923271168, "d2h_bytes_per_step": 638058496,
+                      "steps": 5, "path": "p" * 90},
+              "gpu_launches": 2600, "launch": "each step replays a CUDA graph of its launches",
+              "clocks": {"sm_mhz": 1965, "sm_max_mhz": 1965, "reasons": ["sw_power_cap"], "samples": 5},
+              "cpu_baseline": {"value": 0.056148, "unit": "TFLOP/s", "cores": 16, "kind": "oracle", "sample": "s" * 140},
+              "workloads": {key: {"workload": "w" * 120, "value": 1234.56, "unit": "TFLOP/s", "ms_per_step": 0.0187,
+                                  "steps": 30, "l2": "l" * 300, "roofline": roof, "per_problem": [problem] * 6, "clocks": {}}
+                            for key, _, _ in bench.SUB_WORKLOADS}}
+    line = bench.result_line(result)
+    assert len(json.dumps(line)) < 2800 < len(json.dumps(result))
+    assert set(result) - set(line) == {"per_problem"}
+    for key in ("metric", "value", "config", "e2e", "gpu_launches", "clocks", "cpu_baseline", "vs_baseline"):
+        assert line[key] == result[key]
+    assert line["roofline"]["frac"] == 0.5582 and line["roofline"]["traffic"] == 311666176.0
+    assert {k: w["value"] for k, w in line["workloads"].items()} == {k: 1234.56 for k in result["workloads"]}
