@@ -271,8 +271,9 @@ __global__ void __launch_bounds__(NORM_MAX_THREADS) layer_norm_kernel(const Norm
 // COLS_VECTORS: K is a whole number of 16-byte vectors; a thread owns vectors of V columns, copies and reads its own
 // only, and the ring needs no barrier. COLS_EXACT: and K = N·blockDim.x, so that nothing needs a bounds check (the
 // checks' zero registers and branches were a quarter of the backward pass's instructions). COLS_SINGLE: rows begin
-// anywhere in the tensor (which starts on 16 bytes): a stage takes the 16-byte chunks that hold its row (the bytes behind the tensor's end as zeros), a thread
-// owns single columns blockDim.x apart, and a barrier stands between the copies and the reads.
+// anywhere in the tensor (which starts on 16 bytes): a stage takes the 16-byte chunks that hold its row (the bytes
+// behind the tensor's end as zeros), a thread owns single columns blockDim.x apart, and a barrier stands between the
+// copies and the reads.
 enum : int { COLS_SINGLE = 0, COLS_VECTORS = 1, COLS_EXACT = 2 };
 constexpr int NORM_STAGES = 3, NORM_RING_THREADS = 512;   // 512 threads an SM leave 128 registers each
 
